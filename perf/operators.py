@@ -235,6 +235,7 @@ def _prepare_own(s):
         tabs.accum.copy_(s["accum"])
         s["weights"], s["accum"] = tabs.weights, tabs.accum
         s["tabs"], s["sq"] = tabs, torch.empty(1, dtype=torch.float64, device=DEV)
+        s["sums"] = torch.empty(min(s["ids"].numel(), tabs.total_rows), case["dim"], device=DEV)
         s["table_ws"], s["table_ws_bytes"] = tabs.workspace(case["batch"], s["ids"].numel())
     elif case["op"] == "route":
         e = case["experts"]
@@ -409,11 +410,12 @@ def _own_tables(s):
     b, nnz, ws, n = case["batch"], s["ids"].numel(), s["table_ws"], s["table_ws_bytes"]
     pool = eb.EMB_POOL_MEAN if case["mean"] else eb.EMB_POOL_SUM
     eb.check(eb.emb_bag_prepare(h, s["offsets"], s["ids"], b, nnz, pool, ws, n), "prepare")
-    eb.check(eb.emb_bag_grad_sqnorm_prepared(h, b, nnz, pool, s["grad"], s["sq"], ws, n), "sqnorm")
+    eb.check(eb.emb_bag_grad_reduce_prepared(h, b, nnz, pool, s["grad"], s["sums"], s["sq"], ws, n),
+             "grad_reduce")
     eb.check(eb.emb_clip_grad_norm(s["in_list"], s["out_list"], s["sq"], 1, case["max_norm"],
                                    s["norm"], s["ws"], s["ws_bytes"]), "clip_grad_norm")
-    eb.check(eb.emb_bag_backward_adagrad_clipped_prepared(h, b, nnz, pool, s["grad"], s["norm"][1:],
-                                                          LR, EPS, ws, n), "backward")
+    eb.check(eb.emb_bag_adagrad_reduced_prepared(h, b, nnz, s["sums"], s["norm"][1:], LR, EPS, ws,
+                                                 n), "adagrad_reduced")
     return [s["norm"][0], s["norm"][1], s["out"], s["weights"], s["accum"]]
 
 
