@@ -559,6 +559,154 @@ emb_status_t emb_quantize_rows_int8(const float* x, int64_t rows, int32_t dim, i
 emb_status_t emb_dequantize_rows_int8(const int8_t* codes, const float* scales, int64_t rows,
                                       int32_t dim, float* y, void* stream);
 
+/* ---------------------------------------------------------------- dense operators
+ * What a training step runs beside the tables: the global gradient norm and
+ * its clip, the routing of samples to experts of the dense part, and the norms
+ * around a residual block.  Common to all of them: device pointers unless
+ * marked HOST, tensors contiguous and aligned to their element; rows may have
+ * any width in the stated range, odd ones too.  Arithmetic is in fp32 or wider
+ * and each stored value is rounded once.  The calls are asynchronous on
+ * `stream` (a hipStream_t; NULL is the null stream), allocate nothing, keep
+ * nothing from one call to the next, can be captured into a graph, and give
+ * the same bits on the same inputs.  Workspaces are 256-byte aligned and may
+ * hold anything.  Argument errors enqueue nothing: EMB_ERR_INVALID_ARG for
+ * null or misaligned pointers, sizes, types or kinds out of range,
+ * EMB_ERR_WORKSPACE for a missing, misaligned or short workspace, EMB_ERR_HIP
+ * if a launch fails. */
+typedef enum { EMB_F32 = 0, EMB_BF16 = 1, EMB_F16 = 2 } emb_dtype_t;
+
+typedef struct {
+  void* data;     /* device; may be NULL when numel is 0 */
+  int64_t numel;  /* 0 <= numel < 2^40 */
+  int32_t dtype;  /* emb_dtype_t */
+  int32_t reserved;
+} emb_tensor_t;
+
+/* Global norm of a list of gradients, and the list scaled to at most max_norm:
+ *   norm = sqrt(sum of the squares of every element + sum of extra_sq)
+ *   coef = min(1, max_norm / (norm + 1e-6)); 0 when the norm is not finite
+ *   out[i] = grads[i] * coef; zeros when coef is 0 (a step whose gradients
+ *            hold an infinity or a NaN changes nothing)
+ *   norm_out[0] = norm, norm_out[1] = coef
+ * Squares and their sum are formed in 64 bits.
+ *   grads     HOST [num_tensors]
+ *   out       HOST [num_tensors], numel as in grads, fp32 or the gradient's
+ *             type; out[i].data may be grads[i].data for the same type, and
+ *             must not overlap any gradient otherwise.  NULL: norm and coef
+ *             only
+ *   extra_sq  device fp64 [num_extra], sums of squares formed elsewhere (the
+ *             tables' gradients, other ranks' shares); NULL when num_extra is 0
+ *   max_norm  >= 0, may be infinite
+ *   norm_out  device fp32 [2] */
+size_t emb_grad_workspace_bytes(const emb_tensor_t* grads, int32_t num_tensors);
+emb_status_t emb_clip_grad_norm(const emb_tensor_t* grads, const emb_tensor_t* out,
+                                int32_t num_tensors, const double* extra_sq, int32_t num_extra,
+                                float max_norm, float* norm_out, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/* emb_bag_backward_adagrad_prepared in two parts, with the step of the norm
+ * between them.  emb_bag_grad_reduce_prepared writes the gradient of every
+ * distinct row of the prepared batch, summed over its occurrences:
+ *   sums[u, :] = sum of the row's occurrences' gradients (rows ascending;
+ *                u < the batch's distinct rows, at most min(nnz, sum rows))
+ *   sqnorm[0]  = sum of the squares of all of them, in 64 bits
+ * and emb_bag_adagrad_reduced_prepared steps those rows with scale[0] * sums.
+ *   sums    fp32 [min(nnz, sum rows), D], 16-byte aligned
+ *   sqnorm  device fp64 [1], 8-byte aligned
+ *   scale   device fp32 [1] (norm_out + 1 of emb_clip_grad_norm), NULL: 1.  A
+ *           scale of 0 leaves every row and accumulator as it is, whatever
+ *           the sums hold
+ * The workspace is the prepared one, the same in both calls and untouched
+ * between them.  Errors as emb_bag_backward_adagrad_prepared. */
+emb_status_t emb_bag_grad_reduce_prepared(emb_table_t h, int64_t batch, int64_t nnz,
+                                          emb_pool_t pool, const float* grad_out, float* sums,
+                                          double* sqnorm, void* ws, size_t ws_bytes,
+                                          void* stream);
+emb_status_t emb_bag_adagrad_reduced_prepared(emb_table_t h, int64_t batch, int64_t nnz,
+                                              const float* sums, const float* scale, float lr,
+                                              float eps, void* ws, size_t ws_bytes,
+                                              void* stream);
+
+/* Choices sorted by expert.  Token i (of `tokens`) has topk choices, choice
+ * c = i * topk + j of expert ids[c]; an id outside [0, experts) is no choice
+ * (EMB_ID_ABSENT for a padded token).  The expert-ordered buffer has M rows:
+ *   capacity 0:  M = tokens * topk; expert e's choices take the rows
+ *                offsets[e] .. offsets[e+1]-1 in the order of c, the rest of
+ *                the buffer stays empty;
+ *   capacity C:  M = experts * C; expert e's first C choices take the rows
+ *                from e * C on, its later ones are dropped.
+ *   offsets  int32 [experts + 1], exclusive sums of the kept choices
+ *   src      int32 [M], the choice in each row, -1 for an empty row
+ *   pos      int32 [tokens, topk], the row of each choice, -1 if dropped or none
+ * 1 <= topk <= 64, 1 <= experts <= 1024, tokens * topk and M below 2^31. */
+size_t emb_expert_workspace_bytes(int64_t tokens, int32_t topk, int32_t experts);
+emb_status_t emb_expert_sort(const int64_t* ids, int64_t tokens, int32_t topk, int32_t experts,
+                             int64_t capacity, int32_t* offsets, int32_t* src, int32_t* pos,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/* Rows into expert order and back, with `rows` = M, `dim` values of type
+ * `dtype` per row (8 <= dim <= 2^20) and fp32 weights [tokens, topk]:
+ *   dispatch           xs[r] = x[src[r] / topk], 0 for an empty row
+ *   combine            y[i] = sum over j of weights[i,j] * ys[pos[i,j]], a
+ *                      choice without a row contributing nothing; weights
+ *                      NULL: 1
+ *   combine_backward   dys[r] = weights[src[r]] * dy[src[r] / topk], 0 for an
+ *                      empty row; dweights[i,j] = the dot product of dy[i] and
+ *                      ys[pos[i,j]], 0 for a choice without a row
+ *   dispatch_backward  dx[i] = sum over j of dxs[pos[i,j]]
+ * src and pos are those of emb_expert_sort (a pos outside [0, rows) is taken
+ * as no row).  Outputs must not overlap inputs. */
+emb_status_t emb_expert_dispatch(const void* x, const int32_t* pos, const int32_t* src,
+                                 int64_t tokens, int32_t topk, int64_t rows, int32_t dim,
+                                 int32_t dtype, void* xs, void* stream);
+emb_status_t emb_expert_combine(const void* ys, const int32_t* pos, const float* weights,
+                                int64_t tokens, int32_t topk, int64_t rows, int32_t dim,
+                                int32_t dtype, void* y, void* stream);
+emb_status_t emb_expert_combine_backward(const void* dy, const void* ys, const int32_t* pos,
+                                         const int32_t* src, const float* weights,
+                                         int64_t tokens, int32_t topk, int64_t rows, int32_t dim,
+                                         int32_t dtype, void* dys, float* dweights,
+                                         void* stream);
+emb_status_t emb_expert_dispatch_backward(const void* dxs, const int32_t* pos, int64_t tokens,
+                                          int32_t topk, int64_t rows, int32_t dim, int32_t dtype,
+                                          void* dx, void* stream);
+
+/* The norms before and after a residual block, fused with its gate and
+ * residual scale.  Per row of `dim` values (8 <= dim <= 8192):
+ *   u = block * rsqrt(mean(block^2) + eps) * w_post     (u = block: w_post NULL)
+ *   a = gate, or sigmoid(gate)                          (a = 1: EMB_GATE_NONE)
+ *   y = x + scale * a * u
+ *   h = y * rsqrt(mean(y^2) + eps) * w_pre
+ * y is the residual stream, h the next block's input (formed from y before it
+ * is rounded).  x, block, y, h: [rows, dim] of `dtype`; gate: [rows]
+ * (EMB_GATE_ROW) or [rows, dim] (EMB_GATE_ELEMENT) of `dtype`; w_post, scale,
+ * w_pre: fp32 [dim], 4-byte aligned.  gate_kind: EMB_GATE_NONE, _ROW or
+ * _ELEMENT, with EMB_GATE_SIGMOID or'ed in for a sigmoid.  eps >= 0.  y may be
+ * x; other outputs must not overlap inputs or each other.
+ *
+ * The backward takes y as the forward stored it, and dL/dy (the residual's)
+ * and dL/dh, and writes the gradients of x, block, gate (NULL without one) in
+ * `dtype`, dx being that of x, and those of w_post (NULL without one), scale
+ * and w_pre in fp32 [dim].  dx may be dy.  rows = 0 gives zero weight
+ * gradients. */
+enum {
+  EMB_GATE_NONE = 0,
+  EMB_GATE_ROW = 1,
+  EMB_GATE_ELEMENT = 2,
+  EMB_GATE_SIGMOID = 4
+};
+emb_status_t emb_gated_norm_forward(const void* x, const void* block, const void* gate,
+                                    const float* w_post, const float* scale, const float* w_pre,
+                                    int64_t rows, int32_t dim, int32_t dtype, int32_t gate_kind,
+                                    float eps, void* y, void* h, void* stream);
+size_t emb_gated_norm_workspace_bytes(int64_t rows, int32_t dim);
+emb_status_t emb_gated_norm_backward(const void* y, const void* block, const void* gate,
+                                     const float* w_post, const float* scale, const float* w_pre,
+                                     const void* dy, const void* dh, int64_t rows, int32_t dim,
+                                     int32_t dtype, int32_t gate_kind, float eps, void* dx,
+                                     void* dblock, void* dgate, float* dw_post, float* dscale,
+                                     float* dw_pre, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,6 +6,7 @@
 #include <mutex>
 #include <new>
 
+#include "dense.hpp"
 #include "embtab_internal.hpp"
 #include "interact.hpp"
 
@@ -601,6 +602,46 @@ emb_status_t emb_bag_backward_adagrad_decay_prepared(emb_table_t t, int64_t batc
   dec.log2_rho = (float)std::log2((double)rho);
   dec.period = period;
   return backward_prepared(t, batch, nnz, pool, grad_out, lr, eps, ws, ws_bytes, stream, dec);
+}
+
+emb_status_t emb_bag_grad_reduce_prepared(emb_table_t t, int64_t batch, int64_t nnz,
+                                          emb_pool_t pool, const float* grad_out, float* sums,
+                                          double* sqnorm, void* ws, size_t ws_bytes,
+                                          void* stream) {
+  if (!t || !grad_out || !sqnorm || (nnz > 0 && !sums)) return EMB_ERR_INVALID_ARG;
+  if (pool != EMB_POOL_SUM && pool != EMB_POOL_MEAN) return EMB_ERR_INVALID_ARG;
+  if (batch < 0 || nnz < 0) return EMB_ERR_INVALID_ARG;
+  if (!aligned16(grad_out) || !aligned16(sums) || (reinterpret_cast<uintptr_t>(sqnorm) & 7u) != 0)
+    return EMB_ERR_INVALID_ARG;
+  Plan p;
+  if (!make_plan(t->h, batch, nnz, &p)) return EMB_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < p.total || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return EMB_ERR_WORKSPACE;
+  uint32_t *keys = nullptr, *vals = nullptr;
+  char* w = static_cast<char*>(ws);
+  sorted_arrays(t->h, p, w, &keys, &vals);
+  return hip_status(launch_grad_reduce(t->h, p, keys, vals, pool == EMB_POOL_MEAN, grad_out, sums,
+                                       sqnorm, w, static_cast<hipStream_t>(stream)));
+}
+
+emb_status_t emb_bag_adagrad_reduced_prepared(emb_table_t t, int64_t batch, int64_t nnz,
+                                              const float* sums, const float* scale, float lr,
+                                              float eps, void* ws, size_t ws_bytes,
+                                              void* stream) {
+  if (!t || (nnz > 0 && !sums)) return EMB_ERR_INVALID_ARG;
+  if (!std::isfinite(lr) || !std::isfinite(eps) || eps < 0.0f) return EMB_ERR_INVALID_ARG;
+  if (batch < 0 || nnz < 0) return EMB_ERR_INVALID_ARG;
+  if (!aligned16(sums) || (reinterpret_cast<uintptr_t>(scale) & 3u) != 0)
+    return EMB_ERR_INVALID_ARG;
+  Plan p;
+  if (!make_plan(t->h, batch, nnz, &p)) return EMB_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < p.total || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return EMB_ERR_WORKSPACE;
+  uint32_t *keys = nullptr, *vals = nullptr;
+  char* w = static_cast<char*>(ws);
+  sorted_arrays(t->h, p, w, &keys, &vals);
+  return hip_status(launch_adagrad_rows(t->h, p, keys, sums, scale, lr, eps, w,
+                                        static_cast<hipStream_t>(stream)));
 }
 
 emb_status_t emb_debug_sort_unique(emb_table_t t, const int64_t* offsets, const int64_t* ids,

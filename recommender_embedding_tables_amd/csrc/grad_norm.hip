@@ -1,0 +1,256 @@
+// Global norm of a list of gradients and the list scaled by it, for gfx950.
+//
+//   norm = sqrt(sum_i sum_k g_i[k]^2 + sum_e extra[e])
+//   coef = min(1, max_norm / (norm + 1e-6)), 0 when the norm is not finite
+//   out_i = g_i * coef (0 when coef is 0, whatever the gradient holds)
+//
+// The squares are formed and summed in 64 bits, so a gradient of 1e-30 or 1e30
+// neither vanishes nor overflows, and a list of any length keeps its small
+// members.
+//
+// Bound by memory: the sum reads every gradient, the scale reads it again and
+// writes it, since no element can be scaled before the last one is summed.
+//
+// The list is cut into chunks of kClipChunk elements of one tensor; the tensor
+// table travels as a kernel argument (kClipItems tensors to a launch), so no
+// copy to the device is made and the calls can be captured into a graph.  The
+// partial sums are combined in a fixed order: the result does not depend on
+// the order in which blocks run.
+#include "dense.hpp"
+
+namespace embtab {
+
+namespace {
+
+constexpr int kClipThreads = 256;
+constexpr int kClipChunk = 8192;
+constexpr int kClipItems = 120;     // 32 bytes each: the table stays under 4 KiB
+constexpr int kClipParts = 1024;    // blocks (and partial sums) of one sum launch
+
+struct ClipItem {
+  const void* in;
+  void* out;
+  int64_t n;
+  uint32_t first;  // chunks of the items before
+  uint32_t types;  // input type | output type << 8
+};
+struct ClipList {
+  ClipItem item[kClipItems];
+  uint32_t count, chunks;
+};
+
+__device__ inline uint32_t find_item(const ClipList& l, uint32_t chunk) {
+  uint32_t lo = 0, hi = l.count - 1;  // last item with first <= chunk (no item is empty)
+  while (lo < hi) {
+    const uint32_t mid = (lo + hi + 1) >> 1;
+    if (l.item[mid].first <= chunk) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ inline double wave_sum(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// Sum over the block, valid in every thread.
+__device__ inline double block_sum(double v, double* lds4) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63u) == 0u) lds4[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (lds4[0] + lds4[1]) + (lds4[2] + lds4[3]);
+}
+
+template <class T>
+__device__ inline double chunk_square_sum(const T* p, int64_t len) {
+  constexpr int N = kVec<T>;
+  constexpr int U = kClipChunk / (kClipThreads * N);
+  double acc = 0.0;
+  if (len == kClipChunk) {
+    Raw<T> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = load_raw<T>(p + (u * kClipThreads + threadIdx.x) * N);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const double g = (double)r[u].get(i);
+        acc = __builtin_fma(g, g, acc);
+      }
+    return acc;
+  }
+  const int n = (int)len;
+  for (int k = threadIdx.x * N; k + N <= n; k += kClipThreads * N) {
+    const Raw<T> r = load_raw<T>(p + k);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const double g = (double)r.get(i);
+      acc = __builtin_fma(g, g, acc);
+    }
+  }
+  const int k = n / N * N + (int)threadIdx.x;  // the last n % N elements
+  if (k < n) {
+    const double g = (double)to_f32(p[k]);
+    acc = __builtin_fma(g, g, acc);
+  }
+  return acc;
+}
+
+__global__ __launch_bounds__(kClipThreads) void k_grad_square_sum(const ClipList l,
+                                                                  double* __restrict__ parts) {
+  __shared__ double lds4[4];
+  double acc = 0.0;
+  for (uint32_t c = blockIdx.x; c < l.chunks; c += gridDim.x) {
+    const ClipItem& it = l.item[find_item(l, c)];
+    const int64_t at = (int64_t)(c - it.first) * kClipChunk;
+    const int64_t len = it.n - at < kClipChunk ? it.n - at : kClipChunk;
+    switch (it.types & 0xFFu) {
+      case EMB_F32: acc += chunk_square_sum(static_cast<const float*>(it.in) + at, len); break;
+      case EMB_BF16: acc += chunk_square_sum(static_cast<const bf16_t*>(it.in) + at, len); break;
+      default: acc += chunk_square_sum(static_cast<const f16_t*>(it.in) + at, len); break;
+    }
+  }
+  acc = block_sum(acc, lds4);
+  if (threadIdx.x == 0) parts[blockIdx.x] = acc;
+}
+
+__global__ __launch_bounds__(kClipThreads) void k_clip_coef(const double* __restrict__ parts,
+                                                            uint32_t num_parts,
+                                                            const double* __restrict__ extra,
+                                                            int32_t num_extra, float max_norm,
+                                                            float* __restrict__ norm_out) {
+  __shared__ double lds4[4];
+  double acc = 0.0;
+  for (uint32_t i = threadIdx.x; i < num_parts; i += kClipThreads) acc += parts[i];
+  for (int32_t i = threadIdx.x; i < num_extra; i += kClipThreads) acc += extra[i];
+  acc = block_sum(acc, lds4);
+  if (threadIdx.x == 0) {
+    const double norm = sqrt(acc);
+    double c = (double)max_norm / (norm + 1e-6);
+    c = c < 1.0 ? c : 1.0;
+    norm_out[0] = (float)norm;
+    norm_out[1] = __builtin_isfinite(norm) ? (float)c : 0.0f;
+  }
+}
+
+// Elements of one access: 16 bytes of the wider of the two types.
+template <class TI, class TO>
+constexpr int kScaleVec = 16 / (int)(sizeof(TI) > sizeof(TO) ? sizeof(TI) : sizeof(TO));
+
+template <class TI, class TO, int N>
+__device__ inline Raw<TO, N> scaled(const Raw<TI, N>& r, float c) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = c == 0.0f ? 0.0f : r.get(i) * c;
+  Raw<TO, N> o;
+  o.set_all(v);
+  return o;
+}
+
+template <class TI, class TO>
+__device__ inline void chunk_scale(const TI* p, TO* q, int64_t len, float c) {
+  constexpr int N = kScaleVec<TI, TO>;
+  constexpr int U = kClipChunk / (kClipThreads * N);
+  if (len == kClipChunk) {
+    Raw<TI, N> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      r[u] = load_raw<TI, N, true>(p + (u * kClipThreads + threadIdx.x) * N);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      store_raw<TO, N, true>(q + (u * kClipThreads + threadIdx.x) * N,
+                             scaled<TI, TO, N>(r[u], c));
+    return;
+  }
+  const int n = (int)len;
+  for (int k = threadIdx.x * N; k + N <= n; k += kClipThreads * N)
+    store_raw<TO, N>(q + k, scaled<TI, TO, N>(load_raw<TI, N>(p + k), c));
+  const int k = n / N * N + (int)threadIdx.x;
+  if (k < n) q[k] = from_f32<TO>(c == 0.0f ? 0.0f : to_f32(p[k]) * c);
+}
+
+template <class TI>
+__device__ inline void scale_item(const ClipItem& it, int64_t at, int64_t len, float c) {
+  const TI* p = static_cast<const TI*>(it.in) + at;
+  switch (it.types >> 8) {
+    case EMB_F32: chunk_scale(p, static_cast<float*>(it.out) + at, len, c); break;
+    case EMB_BF16: chunk_scale(p, static_cast<bf16_t*>(it.out) + at, len, c); break;
+    default: chunk_scale(p, static_cast<f16_t*>(it.out) + at, len, c); break;
+  }
+}
+
+__global__ __launch_bounds__(kClipThreads) void k_clip_scale(const ClipList l,
+                                                             const float* __restrict__ norm) {
+  const float c = norm[1];
+  const uint32_t chunk = l.chunks - 1u - blockIdx.x;
+  const ClipItem& it = l.item[find_item(l, chunk)];
+  if (it.in == it.out && c == 1.0f) return;  // in place and not clipped: already there
+  const int64_t at = (int64_t)(chunk - it.first) * kClipChunk;
+  const int64_t len = it.n - at < kClipChunk ? it.n - at : kClipChunk;
+  switch (it.types & 0xFFu) {
+    case EMB_F32: scale_item<float>(it, at, len, c); break;
+    case EMB_BF16: scale_item<bf16_t>(it, at, len, c); break;
+    default: scale_item<f16_t>(it, at, len, c); break;
+  }
+}
+
+// Fills `l` from the list's tensors at `*at` on; advances *at past them.
+bool next_list(const emb_tensor_t* grads, const emb_tensor_t* out, int32_t n, int32_t* at,
+               ClipList* l) {
+  l->count = l->chunks = 0;
+  for (; *at < n && l->count < (uint32_t)kClipItems; ++*at) {
+    const emb_tensor_t& g = grads[*at];
+    if (g.numel == 0) continue;
+    const int64_t chunks = (g.numel + kClipChunk - 1) / kClipChunk;
+    if ((int64_t)l->chunks + chunks > 0x7FFFFFFF) break;  // the next launch takes it
+    ClipItem& it = l->item[l->count++];
+    it.in = g.data;
+    it.out = out ? out[*at].data : nullptr;
+    it.n = g.numel;
+    it.first = l->chunks;
+    it.types = (uint32_t)g.dtype | (uint32_t)(out ? out[*at].dtype : 0) << 8;
+    l->chunks += (uint32_t)chunks;
+  }
+  return l->count != 0;
+}
+
+unsigned sum_blocks(const ClipList& l) {
+  return l.chunks < (unsigned)kClipParts ? l.chunks : (unsigned)kClipParts;
+}
+
+}  // namespace
+
+size_t grad_workspace_bytes(const emb_tensor_t* grads, int32_t n) {
+  ClipList l;
+  int32_t at = 0;
+  size_t parts = 0;
+  while (next_list(grads, nullptr, n, &at, &l)) parts += sum_blocks(l);
+  return (parts * sizeof(double) + 256) & ~(size_t)255;
+}
+
+hipError_t launch_clip_grad_norm(const emb_tensor_t* grads, const emb_tensor_t* out, int32_t n,
+                                 const double* extra, int32_t num_extra, float max_norm,
+                                 float* norm_out, char* ws, hipStream_t s) {
+  double* parts = reinterpret_cast<double*>(ws);
+  ClipList l;
+  int32_t at = 0;
+  uint32_t num_parts = 0;
+  while (next_list(grads, out, n, &at, &l)) {
+    const unsigned grid = sum_blocks(l);
+    hipLaunchKernelGGL(k_grad_square_sum, dim3(grid), dim3(kClipThreads), 0, s, l,
+                       parts + num_parts);
+    num_parts += grid;
+  }
+  hipLaunchKernelGGL(k_clip_coef, dim3(1), dim3(kClipThreads), 0, s, parts, num_parts, extra,
+                     num_extra, max_norm, norm_out);
+  if (out) {
+    at = 0;
+    while (next_list(grads, out, n, &at, &l))
+      hipLaunchKernelGGL(k_clip_scale, dim3(l.chunks), dim3(kClipThreads), 0, s, l, norm_out);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace embtab

@@ -40,6 +40,10 @@ EMB_ID_ABSENT = -2
 EMB_POOL_SUM = 0
 EMB_POOL_MEAN = 1
 
+EMB_F32, EMB_BF16, EMB_F16 = 0, 1, 2
+
+EMB_GATE_NONE, EMB_GATE_ROW, EMB_GATE_ELEMENT, EMB_GATE_SIGMOID = 0, 1, 2, 4
+
 EMB_EMPTY_KEY = 0xFFFFFFFFFFFFFFFF
 
 EXPORTED = [
@@ -56,7 +60,11 @@ EXPORTED = [
     "emb_bag_prepare_ids", "emb_cache_prepare", "emb_stream_copy", "emb_stream_fill",
     "emb_stream_read_sink_floats", "emb_stream_read", "emb_quantize_rows_int8",
     "emb_dequantize_rows_int8", "emb_bag_forward_prepared_int8",
-    "emb_bag_backward_adagrad_prepared_int8",
+    "emb_bag_backward_adagrad_prepared_int8", "emb_grad_workspace_bytes", "emb_clip_grad_norm",
+    "emb_bag_grad_reduce_prepared", "emb_bag_adagrad_reduced_prepared",
+    "emb_expert_workspace_bytes", "emb_expert_sort", "emb_expert_dispatch", "emb_expert_combine",
+    "emb_expert_combine_backward", "emb_expert_dispatch_backward",
+    "emb_gated_norm_workspace_bytes", "emb_gated_norm_forward", "emb_gated_norm_backward",
 ]
 
 EMB_PHASE_FORWARD, EMB_PHASE_KEYS, EMB_PHASE_SORT, EMB_PHASE_UNIQUE = 0, 1, 2, 3
@@ -94,6 +102,15 @@ class emb_tier_desc_t(C.Structure):
         ("host_accum", C.c_void_p),
         ("cache_rows", C.c_int64),
         ("cache_state", C.c_void_p),
+    ]
+
+
+class emb_tensor_t(C.Structure):
+    _fields_ = [
+        ("data", C.c_void_p),
+        ("numel", C.c_int64),
+        ("dtype", C.c_int32),
+        ("reserved", C.c_int32),
     ]
 
 
@@ -157,6 +174,20 @@ def _load():
         "emb_bag_backward_adagrad_prepared_int8": (i32, [P, i64, i64, i32, P, P, f32, f32, P, sz,
                                                          P]),
         "emb_dequantize_rows_int8": (i32, [P, P, i64, i32, P, P]),
+        "emb_grad_workspace_bytes": (sz, [P, i32]),
+        "emb_clip_grad_norm": (i32, [P, P, i32, P, i32, f32, P, P, sz, P]),
+        "emb_bag_grad_reduce_prepared": (i32, [P, i64, i64, i32, P, P, P, P, sz, P]),
+        "emb_bag_adagrad_reduced_prepared": (i32, [P, i64, i64, P, P, f32, f32, P, sz, P]),
+        "emb_expert_workspace_bytes": (sz, [i64, i32, i32]),
+        "emb_expert_sort": (i32, [P, i64, i32, i32, i64, P, P, P, P, sz, P]),
+        "emb_expert_dispatch": (i32, [P, P, P, i64, i32, i64, i32, i32, P, P]),
+        "emb_expert_combine": (i32, [P, P, P, i64, i32, i64, i32, i32, P, P]),
+        "emb_expert_combine_backward": (i32, [P, P, P, P, P, i64, i32, i64, i32, i32, P, P, P]),
+        "emb_expert_dispatch_backward": (i32, [P, P, i64, i32, i64, i32, i32, P, P]),
+        "emb_gated_norm_workspace_bytes": (sz, [i64, i32]),
+        "emb_gated_norm_forward": (i32, [P, P, P, P, P, P, i64, i32, i32, i32, f32, P, P, P]),
+        "emb_gated_norm_backward": (i32, [P, P, P, P, P, P, P, P, i64, i32, i32, i32, f32, P, P,
+                                          P, P, P, P, P, sz, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -514,3 +545,112 @@ def emb_bag_backward_adagrad_prepared_int8(handle, batch, nnz, pool, grad_codes,
 def emb_dequantize_rows_int8(codes, scales, rows, dim, y, stream=None) -> int:
     return _lib.emb_dequantize_rows_int8(_ptr(codes), _ptr(scales), rows, dim, _ptr(y),
                                          _stream(stream))
+
+
+_DTYPE_CODES = {"torch.float32": EMB_F32, "torch.bfloat16": EMB_BF16, "torch.float16": EMB_F16}
+
+
+def dtype_code(dtype) -> int:
+    """EMB_F32, EMB_BF16 or EMB_F16 of a torch dtype; ValueError for another one."""
+    try:
+        return _DTYPE_CODES[str(dtype)]
+    except KeyError:
+        raise ValueError(f"{dtype}: float32, bfloat16 or float16 is wanted") from None
+
+
+class TensorList:
+    """The HOST array of emb_tensor_t that emb_clip_grad_norm takes, over contiguous torch
+    tensors, which it keeps alive.  Made once for the buffers a program keeps."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self.array = (emb_tensor_t * max(1, len(self.tensors)))()
+        for item, t in zip(self.array, self.tensors):
+            if not t.is_contiguous():
+                raise ValueError(f"a tensor of shape {tuple(t.shape)} is not contiguous")
+            item.data, item.numel, item.dtype = t.data_ptr(), t.numel(), dtype_code(t.dtype)
+        self.ptr = C.addressof(self.array)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def emb_grad_workspace_bytes(grads: TensorList) -> int:
+    return int(_lib.emb_grad_workspace_bytes(grads.ptr, len(grads)))
+
+
+def emb_clip_grad_norm(grads: TensorList, out, extra_sq, num_extra, max_norm, norm_out, ws,
+                       ws_bytes, stream=None) -> int:
+    """out: a TensorList as long as grads, or None (norm and coefficient only)."""
+    if out is not None and len(out) != len(grads):
+        return EMB_ERR_INVALID_ARG
+    return _lib.emb_clip_grad_norm(grads.ptr, out.ptr if out is not None else None, len(grads),
+                                   _ptr(extra_sq), num_extra, max_norm, _ptr(norm_out), _ptr(ws),
+                                   ws_bytes, _stream(stream))
+
+
+def emb_bag_grad_reduce_prepared(handle, batch, nnz, pool, grad_out, sums, sqnorm, ws, ws_bytes,
+                                 stream=None) -> int:
+    return _lib.emb_bag_grad_reduce_prepared(handle, batch, nnz, pool, _ptr(grad_out),
+                                             _ptr(sums), _ptr(sqnorm), _ptr(ws), ws_bytes,
+                                             _stream(stream))
+
+
+def emb_bag_adagrad_reduced_prepared(handle, batch, nnz, sums, scale, lr, eps, ws, ws_bytes,
+                                     stream=None) -> int:
+    return _lib.emb_bag_adagrad_reduced_prepared(handle, batch, nnz, _ptr(sums), _ptr(scale), lr,
+                                                 eps, _ptr(ws), ws_bytes, _stream(stream))
+
+
+def emb_expert_workspace_bytes(tokens, topk, experts) -> int:
+    return int(_lib.emb_expert_workspace_bytes(tokens, topk, experts))
+
+
+def emb_expert_sort(ids, tokens, topk, experts, capacity, offsets, src, pos, ws, ws_bytes,
+                    stream=None) -> int:
+    return _lib.emb_expert_sort(_ptr(ids), tokens, topk, experts, capacity, _ptr(offsets),
+                                _ptr(src), _ptr(pos), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def emb_expert_dispatch(x, pos, src, tokens, topk, rows, dim, dtype, xs, stream=None) -> int:
+    return _lib.emb_expert_dispatch(_ptr(x), _ptr(pos), _ptr(src), tokens, topk, rows, dim, dtype,
+                                    _ptr(xs), _stream(stream))
+
+
+def emb_expert_combine(ys, pos, weights, tokens, topk, rows, dim, dtype, y, stream=None) -> int:
+    return _lib.emb_expert_combine(_ptr(ys), _ptr(pos), _ptr(weights), tokens, topk, rows, dim,
+                                   dtype, _ptr(y), _stream(stream))
+
+
+def emb_expert_combine_backward(dy, ys, pos, src, weights, tokens, topk, rows, dim, dtype, dys,
+                                dweights, stream=None) -> int:
+    return _lib.emb_expert_combine_backward(_ptr(dy), _ptr(ys), _ptr(pos), _ptr(src),
+                                            _ptr(weights), tokens, topk, rows, dim, dtype,
+                                            _ptr(dys), _ptr(dweights), _stream(stream))
+
+
+def emb_expert_dispatch_backward(dxs, pos, tokens, topk, rows, dim, dtype, dx,
+                                 stream=None) -> int:
+    return _lib.emb_expert_dispatch_backward(_ptr(dxs), _ptr(pos), tokens, topk, rows, dim, dtype,
+                                             _ptr(dx), _stream(stream))
+
+
+def emb_gated_norm_workspace_bytes(rows, dim) -> int:
+    return int(_lib.emb_gated_norm_workspace_bytes(rows, dim))
+
+
+def emb_gated_norm_forward(x, block, gate, w_post, scale, w_pre, rows, dim, dtype, gate_kind, eps,
+                           y, h, stream=None) -> int:
+    return _lib.emb_gated_norm_forward(_ptr(x), _ptr(block), _ptr(gate), _ptr(w_post),
+                                       _ptr(scale), _ptr(w_pre), rows, dim, dtype, gate_kind, eps,
+                                       _ptr(y), _ptr(h), _stream(stream))
+
+
+def emb_gated_norm_backward(y, block, gate, w_post, scale, w_pre, dy, dh, rows, dim, dtype,
+                            gate_kind, eps, dx, dblock, dgate, dw_post, dscale, dw_pre, ws,
+                            ws_bytes, stream=None) -> int:
+    return _lib.emb_gated_norm_backward(_ptr(y), _ptr(block), _ptr(gate), _ptr(w_post),
+                                        _ptr(scale), _ptr(w_pre), _ptr(dy), _ptr(dh), rows, dim,
+                                        dtype, gate_kind, eps, _ptr(dx), _ptr(dblock),
+                                        _ptr(dgate), _ptr(dw_post), _ptr(dscale), _ptr(dw_pre),
+                                        _ptr(ws), ws_bytes, _stream(stream))

@@ -1,0 +1,727 @@
+"""The dense operators against plain 64-bit forms of their formulas.
+
+Tolerances are first-order error bounds counted from the formulas, with
+U = 2^-24 the rounding of fp32 and half(t) that of the stored type; every
+bound is computed in 64 bits from the inputs (see each test)."""
+import numpy as np
+import pytest
+import torch
+
+from recommender_embedding_tables_amd import synth
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+from recommender_embedding_tables_amd import embtab as eb  # noqa: E402
+
+DEV = torch.device("cuda")
+U = 2.0 ** -24
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+TINY = {torch.float32: 2.0 ** -149, torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -24}
+
+
+def half(t):
+    return torch.finfo(t).eps / 2
+
+
+def within(got, ref, bound, what):
+    """|got - ref| <= bound + the storage rounding of ref (subnormal steps included)."""
+    t = got.dtype
+    err = (got.double() - ref).abs()
+    lim = bound + (half(t) * (ref.abs() + bound) if t != torch.float64 else 0) + \
+        TINY.get(t, 0.0)
+    assert torch.isfinite(got).all(), what
+    assert (err <= lim).all(), f"{what}: worst {float((err / lim).max()):.3g} of the bound"
+
+
+def rand(g, *shape, scale=1.0):
+    return torch.randn(*shape, generator=g, device=DEV) * scale
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def guarded(shape, dtype, pad=64, shift=0):
+    """A tensor of `shape` inside a larger one filled with a marker; `shift` elements off
+    the allocation's alignment.  Returns (tensor, check())."""
+    n = int(np.prod(shape))
+    base = torch.full((pad + shift + n + pad,), 77, dtype=dtype, device=DEV)
+    view = base[pad + shift:pad + shift + n].view(shape)
+
+    def check():
+        assert (base[:pad + shift] == 77).all() and (base[pad + shift + n:] == 77).all(), \
+            "written outside the output"
+    return view, check
+
+
+# ---------------------------------------------------------------- clip
+
+def run_clip(grads, out_dtypes, max_norm, extra=None, in_place=False):
+    outs = grads if in_place else [torch.empty_like(x, dtype=t) for x, t in zip(grads, out_dtypes)]
+    gl, ol = eb.TensorList(grads), eb.TensorList(outs)
+    need = eb.emb_grad_workspace_bytes(gl)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV).fill_(255)
+    norm = torch.empty(2, device=DEV)
+    eb.check(eb.emb_clip_grad_norm(gl, ol, extra, 0 if extra is None else extra.numel(), max_norm,
+                                   norm, ws, need), "clip")
+    torch.cuda.synchronize()
+    return norm, outs
+
+
+def plain_clip(grads, max_norm, extra=None):
+    sq = sum(float((x.double() ** 2).sum()) for x in grads)
+    if extra is not None:
+        sq += float(extra.sum())
+    norm = sq ** 0.5
+    return norm, min(1.0, max_norm / (norm + 1e-6))
+
+
+SIZES = [[1], [7, 1, 8, 9], [8192], [8191, 8193, 0, 5], [1, 3, 65537, 16384, 2, 31],
+         [3_000_001, 17], [9] * 250]
+
+
+@pytest.mark.parametrize("sizes", SIZES, ids=lambda s: f"{len(s)}x{max(s)}")
+@pytest.mark.parametrize("kind,same", [("f32", True), ("bf16", True), ("f16", False),
+                                       ("mixed", False), ("mixed", True)])
+@pytest.mark.parametrize("max_norm", [0.5, 1e9])
+def test_clip(sizes, kind, same, max_norm):
+    g = gen(sum(sizes) + len(kind))
+    ts = [TYPES[kind] if kind != "mixed" else list(TYPES.values())[i % 3]
+          for i in range(len(sizes))]
+    # one element off the allocation's alignment, each tensor
+    grads = [rand(g, n + 1, scale=0.1).to(t)[1:] for n, t in zip(sizes, ts)]
+    extra = torch.tensor([0.25, 3.0], dtype=torch.float64, device=DEV) if len(sizes) % 2 else None
+    ref, coef = plain_clip(grads, max_norm, extra)
+    norm, outs = run_clip(grads, [t if same else torch.float32 for t in ts], max_norm, extra)
+    # 64-bit sums: the norm and the coefficient are one fp32 rounding off
+    assert abs(float(norm[0]) - ref) <= 1.01 * U * ref
+    assert abs(float(norm[1]) - coef) <= 1.01 * U * coef
+    for x, o in zip(grads, outs):  # the coefficient's rounding and the product's
+        r = x.double() * coef
+        within(o, r, 2.02 * U * r.abs() + TINY[torch.float32], "scaled")
+    again, outs2 = run_clip(grads, [t if same else torch.float32 for t in ts], max_norm, extra)
+    assert torch.equal(again, norm) and all(torch.equal(a, b) for a, b in zip(outs, outs2))
+
+
+@pytest.mark.parametrize("max_norm", [0.5, 1e9])
+def test_clip_in_place_and_norm_only(max_norm):
+    g = gen(5)
+    grads = [rand(g, n).to(t) for n, t in ((70_001, torch.float32), (9, torch.bfloat16),
+                                           (20_000, torch.float16))]
+    norm_a, outs = run_clip(grads, [x.dtype for x in grads], max_norm)
+    copies = [x.clone() for x in grads]
+    norm_b, _ = run_clip(copies, None, max_norm, in_place=True)
+    assert torch.equal(norm_a, norm_b)
+    assert all(torch.equal(a, b) for a, b in zip(outs, copies))
+    gl = eb.TensorList(grads)
+    need = eb.emb_grad_workspace_bytes(gl)
+    norm_c = torch.empty(2, device=DEV)
+    eb.check(eb.emb_clip_grad_norm(gl, None, None, 0, max_norm, norm_c,
+                                   torch.empty(need, dtype=torch.uint8, device=DEV), need), "norm")
+    assert torch.equal(norm_a, norm_c)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_clip_of_a_gradient_that_is_not_finite(value):
+    x = torch.ones(10_000, device=DEV)
+    x[1234] = value
+    norm, outs = run_clip([x, torch.ones(3, device=DEV).bfloat16()],
+                          [torch.float32, torch.bfloat16], 1.0)
+    assert not torch.isfinite(norm[0]) and float(norm[1]) == 0.0
+    assert all((o == 0).all() for o in outs)
+
+
+def test_clip_wide_range_and_empty():
+    # squares beyond fp32's range on both sides; a list with no element
+    norm, outs = run_clip([torch.full((4,), 1e30, device=DEV), torch.full((9,), 1e-30, device=DEV)],
+                          [torch.float32] * 2, 1.0)
+    assert abs(float(norm[0]) - 2e30) <= 1e-6 * 2e30
+    norm, _ = run_clip([torch.full((16,), 1e-30, device=DEV)], [torch.float32], 1.0)
+    assert abs(float(norm[0]) - 4e-30) <= 1e-6 * 4e-30 and float(norm[1]) == 1.0
+    for grads in ([], [torch.empty(0, device=DEV)]):
+        norm, _ = run_clip(grads, [torch.float32] * len(grads), 1.0)
+        assert norm.tolist() == [0.0, 1.0]
+    norm, outs = run_clip([torch.ones(5, device=DEV)], [torch.float32], 0.0)
+    assert float(norm[1]) == 0.0 and (outs[0] == 0).all()
+
+
+# ---------------------------------------------------------------- tables
+
+def t_(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def plain_table_sums(rows, D, offsets, ids, B, mean, grad):
+    """(touched global rows ascending, sums, sums of absolute terms, occurrences), 64 bits."""
+    start = np.concatenate([[0], np.cumsum(rows)])
+    lens = np.diff(offsets)
+    bag = np.repeat(np.arange(lens.size), lens)
+    table, sample = bag // B, bag % B
+    ok = (ids >= 0) & (ids < np.asarray(rows)[table])
+    grow = (start[table] + ids)[ok]
+    per = grad.astype(np.float64)[sample[ok], table[ok]]
+    if mean:
+        per = per / lens[bag[ok]][:, None]
+    uniq, inv, cnt = np.unique(grow, return_inverse=True, return_counts=True)
+    s, a = np.zeros((uniq.size, D)), np.zeros((uniq.size, D))
+    np.add.at(s, inv, per)
+    np.add.at(a, inv, np.abs(per))
+    return uniq, s, a, cnt
+
+
+TABLES = [  # rows, D, B, longest bag, share of ids without a row
+    ([1], 4, 1, 1, 0.0),                # one occurrence
+    ([1], 8, 3000, 3, 0.0),             # every occurrence of one row: spans of blocks
+    ([50, 3], 16, 700, 5, 0.1),
+    ([1000, 77, 5000], 32, 257, 6, 0.0),
+    ([2, 300, 20000], 64, 3000, 9, 0.05),
+    ([5, 900], 128, 5000, 1, 0.0),      # one-hot
+    ([40, 3], 256, 600, 20, 0.0),
+    ([64], 1024, 300, 4, 0.0),
+    ([300, 7], 20, 400, 3, 0.3),        # lanes without a column
+]
+
+
+@pytest.mark.parametrize("rows,D,B,bag,absent", TABLES, ids=lambda v: str(v).replace(" ", ""))
+@pytest.mark.parametrize("mean", [False, True])
+def test_table_gradients_in_two_parts(rows, D, B, bag, absent, mean):
+    r = np.random.default_rng(D * 7 + B)
+    T = len(rows)
+    lens = np.ones(T * B, np.int64) if bag == 1 else r.integers(0, bag + 1, T * B)
+    if bag > 1:
+        lens[0] = max(lens[0], 1)
+    offsets = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    table = np.repeat(np.arange(T * B) // B, lens)
+    ids = (r.random(offsets[-1]) ** 3 * np.asarray(rows)[table]).astype(np.int64)
+    ids[r.random(ids.size) < absent] = eb.EMB_ID_ABSENT
+    nnz = ids.size
+    grad = r.standard_normal((B, T, D)).astype(np.float32)
+    uniq, s, a, cnt = plain_table_sums(rows, D, offsets, ids, B, mean, grad)
+    tabs = eb.EmbTables(rows, D, seed=3)
+    pool = eb.EMB_POOL_MEAN if mean else eb.EMB_POOL_SUM
+    ws, need = tabs.workspace(B, nnz)
+    sums, check = guarded((min(nnz, sum(rows)), D), torch.float32)
+    sq = torch.full((1,), -1.0, dtype=torch.float64, device=DEV)
+    d_off, d_ids, d_g = t_(offsets), t_(ids), t_(grad)
+    for _ in range(2):  # the same bits on a used workspace
+        eb.check(eb.emb_bag_prepare(tabs.handle, d_off, d_ids, B, nnz, pool, ws, need), "prepare")
+        eb.check(eb.emb_bag_grad_reduce_prepared(tabs.handle, B, nnz, pool, d_g, sums, sq, ws,
+                                                 need), "reduce")
+        torch.cuda.synchronize()
+        check()
+        first = sums[:uniq.size].clone() if _ == 0 else first
+        sq0 = sq.clone() if _ == 0 else sq0
+    assert torch.equal(first, sums[:uniq.size]) and torch.equal(sq, sq0)
+    # one rounding per added term, two for the mean's scale and product
+    bound = t_((cnt[:, None] + 2) * U * a)
+    within(sums[:uniq.size], t_(s), bound, "sums")
+    S = t_(s)
+    lim = float((2 * S.abs() * (bound + U * S.abs()) + (bound + U * S.abs()) ** 2).sum())
+    assert abs(float(sq) - float((S ** 2).sum())) <= lim + 1e-12 * float((S ** 2).sum())
+    # the step with a scale, by the library's rule: 1e-5 of the terms' sum plus 1e-6
+    W0, G0 = tabs.weights.clone().double(), tabs.accum.clone().double()
+    lr, eps, c = 0.05, 1e-6, 0.37
+    scale = torch.tensor([c], device=DEV)
+    eb.check(eb.emb_bag_adagrad_reduced_prepared(tabs.handle, B, nnz, sums, scale, lr, eps, ws,
+                                                 need), "step")
+    torch.cuda.synchronize()
+    idx = t_(uniq)
+    cf = float(scale[0])
+    G, W = G0.clone(), W0.clone()
+    G[idx] += (cf * S) ** 2
+    W[idx] -= lr * cf * S / (G[idx].sqrt() + eps)
+    terms = cf * t_(a)
+    eG, eW = torch.zeros_like(G), torch.zeros_like(W)
+    eG[idx] = 1e-5 * (G0[idx] + terms ** 2) + 1e-6
+    eW[idx] = 1e-5 * (W0[idx].abs() + lr * terms / (G[idx].sqrt() + eps)) + 1e-6 + \
+        lr * terms / (2 * G[idx] ** 1.5) * eG[idx]
+    assert ((tabs.accum.double() - G).abs() <= eG).all(), "accumulators"
+    assert ((tabs.weights.double() - W).abs() <= eW).all(), "weights"
+    # a scale of 0 changes nothing, whatever the sums hold
+    W1, G1 = tabs.weights.clone(), tabs.accum.clone()
+    sums[:] = float("nan")
+    eb.check(eb.emb_bag_adagrad_reduced_prepared(tabs.handle, B, nnz, sums,
+                                                 torch.zeros(1, device=DEV), lr, eps, ws, need),
+             "step of 0")
+    assert torch.equal(tabs.weights, W1) and torch.equal(tabs.accum, G1)
+    assert eb.emb_status_sync(tabs.handle) == (eb.EMB_OK, 0)
+    tabs.close()
+
+
+def test_two_parts_match_the_fused_step():
+    w = synth.workload(2, T=4, B=5000, D=64, rows=[300, 20000, 4000, 50])
+    offsets, ids = synth.gen_batch(w, 0)
+    B, nnz = w.B, ids.size
+    d_off, d_ids, grad = t_(offsets), t_(ids), t_(synth.gen_grad(w, 0))
+    one, two = (eb.EmbTables(w.rows, w.D, seed=8) for _ in range(2))
+    tiered = eb.EmbTables(w.rows, w.D, seed=8, cache_rows=16384)
+    sq = torch.empty(1, dtype=torch.float64, device=DEV)
+    for _ in range(3):
+        ws, need = one.workspace(B, nnz)
+        eb.check(eb.emb_bag_prepare(one.handle, d_off, d_ids, B, nnz, 0, ws, need), "prepare")
+        eb.check(eb.emb_bag_backward_adagrad_prepared(one.handle, B, nnz, 0, grad, w.lr, w.eps,
+                                                      ws, need), "fused")
+        for tabs in (two, tiered):
+            ws, need = tabs.workspace(B, nnz)
+            sums = torch.empty(min(nnz, tabs.total_rows), w.D, device=DEV)
+            eb.check(eb.emb_bag_prepare(tabs.handle, d_off, d_ids, B, nnz, 0, ws, need), "prepare")
+            eb.check(eb.emb_bag_grad_reduce_prepared(tabs.handle, B, nnz, 0, grad, sums, sq, ws,
+                                                     need), "reduce")
+            eb.check(eb.emb_bag_adagrad_reduced_prepared(tabs.handle, B, nnz, sums, None, w.lr,
+                                                         w.eps, ws, need), "step")
+    torch.cuda.synchronize()
+    # hot rows may be summed in another order than the fused kernel's
+    assert torch.allclose(one.weights, two.weights, rtol=1e-5, atol=1e-6)
+    assert torch.allclose(one.accum, two.accum, rtol=1e-5, atol=1e-6)
+    eb.check(eb.emb_cache_flush(tiered.handle), "flush")
+    torch.cuda.synchronize()
+    assert torch.equal(tiered.host_weights, two.weights.cpu())
+    assert torch.equal(tiered.host_accum, two.accum.cpu())
+    for t in (one, two, tiered):
+        t.close()
+
+
+def test_empty_batches_of_table_gradients():
+    tabs = eb.EmbTables([100, 20], 16, seed=1)
+    W = tabs.weights.clone()
+    sq = torch.full((1,), 5.0, dtype=torch.float64, device=DEV)
+    off, none = torch.zeros(2 * 30 + 1, dtype=torch.int64, device=DEV), None
+    ws, need = tabs.workspace(30, 0)
+    grad = torch.ones(30, 2, 16, device=DEV)
+    eb.check(eb.emb_bag_prepare(tabs.handle, off, none, 30, 0, 0, ws, need), "prepare")
+    eb.check(eb.emb_bag_grad_reduce_prepared(tabs.handle, 30, 0, 0, grad, none, sq, ws, need),
+             "reduce")
+    eb.check(eb.emb_bag_adagrad_reduced_prepared(tabs.handle, 30, 0, none, none, 0.1, 1e-8, ws,
+                                                 need), "step")
+    torch.cuda.synchronize()
+    assert float(sq) == 0.0 and torch.equal(W, tabs.weights)
+    # every id without a row
+    ids = torch.full((60,), eb.EMB_ID_ABSENT, dtype=torch.int64, device=DEV)
+    off = torch.arange(61, dtype=torch.int64, device=DEV)
+    ws, need = tabs.workspace(30, 60)
+    sums, sq[0] = torch.empty(60, 16, device=DEV), 5.0
+    eb.check(eb.emb_bag_prepare(tabs.handle, off, ids, 30, 60, 0, ws, need), "prepare")
+    eb.check(eb.emb_bag_grad_reduce_prepared(tabs.handle, 30, 60, 0, grad, sums, sq, ws, need),
+             "reduce")
+    eb.check(eb.emb_bag_adagrad_reduced_prepared(tabs.handle, 30, 60, sums, none, 0.1, 1e-8, ws,
+                                                 need), "step")
+    torch.cuda.synchronize()
+    assert float(sq) == 0.0 and torch.equal(W, tabs.weights)
+    tabs.close()
+
+
+# ---------------------------------------------------------------- experts
+
+def plain_sort(ids, experts, capacity):
+    """offsets, src, pos of the definition, one choice after another."""
+    n, k = ids.shape
+    flat = ids.reshape(-1)
+    m = capacity * experts if capacity else n * k
+    src, pos = np.full(m, -1, np.int32), np.full(n * k, -1, np.int32)
+    kept, at = [0], 0
+    for e in range(experts):
+        mine = np.flatnonzero(flat == e)
+        mine = mine[:capacity] if capacity else mine
+        rows = (e * capacity if capacity else at) + np.arange(mine.size)
+        src[rows], pos[mine] = mine, rows
+        at += mine.size
+        kept.append(at)
+    return np.array(kept, np.int32), src, pos.reshape(n, k)
+
+
+def sort_on_gpu(ids, experts, capacity):
+    n, k = ids.shape
+    m = capacity * experts if capacity else n * k
+    off, c0 = guarded((experts + 1,), torch.int32)
+    src, c1 = guarded((m,), torch.int32)
+    pos, c2 = guarded((n, k), torch.int32)
+    need = eb.emb_expert_workspace_bytes(n, k, experts)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV).fill_(255)
+    eb.check(eb.emb_expert_sort(t_(ids), n, k, experts, capacity, off, src, pos, ws, need), "sort")
+    torch.cuda.synchronize()
+    for c in (c0, c1, c2):
+        c()
+    return off, src, pos
+
+
+def choices(seed, n, k, experts, absent):
+    r = np.random.default_rng(seed)
+    ids = (r.random((n, k)) ** 2 * experts).astype(np.int64)
+    ids[r.random(n) < absent] = eb.EMB_ID_ABSENT
+    if n:
+        odd = r.random((n, k)) < absent / 4  # ids that name no expert
+        ids[odd] = r.choice([-1, experts, 2**40, -2**40], int(odd.sum()))
+    return ids
+
+
+SORTS = [(0, 1, 3), (1, 1, 1), (1, 8, 8), (64, 2, 8), (511, 2, 16), (512, 2, 16), (513, 2, 16),
+         (5000, 3, 7), (4097, 1, 1024), (70_000, 4, 256), (3, 64, 2), (20_000, 8, 100)]
+
+
+@pytest.mark.parametrize("n,k,experts", SORTS)
+@pytest.mark.parametrize("capacity", [0, 1, "mean"])
+@pytest.mark.parametrize("absent", [0.0, 0.3, 1.0])
+def test_expert_sort(n, k, experts, capacity, absent):
+    ids = choices(n + k, n, k, experts, absent)
+    cap = max(1, n * k // experts) if capacity == "mean" else capacity
+    off, src, pos = sort_on_gpu(ids, experts, cap)
+    for got, ref, what in zip((off, src, pos), plain_sort(ids, experts, cap),
+                              ("offsets", "src", "pos")):
+        assert np.array_equal(got.cpu().numpy(), ref), what
+
+
+ROWS = [  # tokens, topk, experts, capacity, dim, absent
+    (1, 1, 1, 0, 8, 0.0), (3, 2, 4, 0, 9, 0.0), (5, 3, 4, 2, 15, 0.3), (64, 2, 8, 0, 512, 0.0),
+    (257, 4, 16, 40, 479, 0.1), (33, 5, 9, 0, 33, 0.0), (100, 8, 8, 0, 1000, 0.2),
+    (40, 12, 20, 30, 351, 0.1), (7, 2, 3, 5, 3328, 0.0), (17, 6, 6, 0, 4001, 0.5),
+    (9, 2, 2, 0, 20011, 0.0), (20, 2, 4, 0, 64, 1.0),
+]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("n,k,experts,cap,dim,absent", ROWS)
+def test_expert_rows(kind, n, k, experts, cap, dim, absent):
+    t, g = TYPES[kind], gen(n * dim)
+    ids = choices(n + dim, n, k, experts, absent)
+    _, src, pos = sort_on_gpu(ids, experts, cap)
+    m = src.numel()
+    # rows one element off the allocation's alignment
+    x, dy = (rand(g, n * dim + 1).to(t)[1:].view(n, dim) for _ in range(2))
+    ys, dxs = (rand(g, m * dim + 1).to(t)[1:].view(m, dim) for _ in range(2))
+    ys[src < 0] = float("nan")   # empty rows are never read
+    dxs[src < 0] = float("nan")
+    w = torch.softmax(rand(g, n, k), 1)
+    w[pos < 0] = float("nan")    # nor the weights of choices without a row
+    code, args = eb.dtype_code(t), (n, k, m, dim, eb.dtype_code(t))
+    xs, c0 = guarded((m, dim), t, shift=1)
+    y, c1 = guarded((n, dim), t, shift=1)
+    dys, c2 = guarded((m, dim), t, shift=1)
+    dw, c3 = guarded((n, k), torch.float32)
+    dx, c4 = guarded((n, dim), t, shift=1)
+    eb.check(eb.emb_expert_dispatch(x, pos, src, *args, xs), "dispatch")
+    eb.check(eb.emb_expert_combine(ys, pos, w, *args, y), "combine")
+    eb.check(eb.emb_expert_combine_backward(dy, ys, pos, src, w, *args, dys, dw), "backward")
+    eb.check(eb.emb_expert_dispatch_backward(dxs, pos, *args, dx), "dispatch backward")
+    torch.cuda.synchronize()
+    for c in (c0, c1, c2, c3, c4):
+        c()
+    assert code == args[-1]
+    have, tok = src >= 0, (src.clamp(min=0) // k).long()
+    zero = torch.zeros((), dtype=torch.float64, device=DEV)
+    assert torch.equal(xs, torch.where(have[:, None], x[tok], torch.zeros_like(x[:1])))
+    on, at = (pos >= 0), pos.clamp(min=0).long()
+    wd = torch.where(on, w.double(), zero)
+    picked = torch.where(on[..., None], ys[at].double(), zero)          # [n, k, dim]
+    terms = wd[..., None] * picked
+    # one rounding per fused step, k steps
+    within(y, terms.sum(1), k * U * terms.abs().sum(1), "combine")
+    wr = torch.where(have, w.reshape(-1)[src.clamp(min=0).long()].double(), zero)
+    ref = wr[:, None] * dy[tok].double() * have[:, None]
+    within(dys, ref, U * ref.abs(), "dys")
+    assert (dys[~have] == 0).all()
+    prod = dy.double()[:, None, :] * picked
+    # a lane adds its columns one after another, then six steps over the wave
+    steps = -(-dim // (64 * (16 // t.itemsize))) * (16 // t.itemsize) + 6
+    within(dw, prod.sum(2), steps * U * prod.abs().sum(2), "dweights")
+    assert (dw[~on] == 0).all()
+    back = torch.where(on[..., None], dxs[at].double(), zero)
+    within(dx, back.sum(1), k * U * back.abs().sum(1), "dx")
+
+
+def test_a_pos_outside_the_rows_is_no_row():
+    n, k, m, dim = 4, 2, 5, 16
+    x = torch.ones(n, dim, device=DEV)
+    pos = torch.tensor([[0, 5], [1, 2**31 - 1], [-7, 2], [3, 4]], dtype=torch.int32, device=DEV)
+    src = torch.tensor([0, 2, 5, 6, 7], dtype=torch.int32, device=DEV)
+    xs, c0 = guarded((m, dim), torch.float32)
+    y, c1 = guarded((n, dim), torch.float32)
+    eb.check(eb.emb_expert_dispatch(x, pos, src, n, k, m, dim, 0, xs), "dispatch")
+    eb.check(eb.emb_expert_dispatch_backward(xs, pos, n, k, m, dim, 0, y), "back")
+    torch.cuda.synchronize()
+    c0()
+    c1()
+    assert (xs == 1).all() and y[:, 0].tolist() == [1, 1, 1, 2]
+
+
+# ---------------------------------------------------------------- gated norm
+
+def norm_inputs(seed, n, dim, t, gate, post):
+    g = gen(seed)
+
+    def act(scale=1.0):
+        return (rand(g, n * dim + 1, scale=scale).to(t)[1:]).view(n, dim)
+    x, block, dy, dh = act(), act(3.0), act(), act()
+    gt = {"none": None, "row": rand(g, n).to(t), "element": act()}[gate]
+    w_post = 1 + 0.1 * rand(g, dim) if post else None
+    return x, block, gt, w_post, rand(g, dim, scale=0.5), 1 + 0.1 * rand(g, dim), dy, dh
+
+
+def gate_code(gate, sig):
+    c = {"none": eb.EMB_GATE_NONE, "row": eb.EMB_GATE_ROW, "element": eb.EMB_GATE_ELEMENT}[gate]
+    return c | (eb.EMB_GATE_SIGMOID if sig and gate != "none" else 0)
+
+
+def sum_steps(dim, t):
+    """Roundings of a row's sum: at most 16 elements in a thread, 64 lanes, 16 waves."""
+    return 16 + 6 + 16
+
+
+def gate_of(gt, sig):
+    """a, and its relative error (the sigmoid: exp, sum and quotient, two steps each)."""
+    if gt is None:
+        return torch.ones(1, 1, dtype=torch.float64, device=DEV), 0.0
+    a = gt.double() if gt.dim() == 2 else gt.double()[:, None]
+    return (torch.sigmoid(a), 6 * U) if sig else (a, 0.0)
+
+
+def rms_inv(v, eps):
+    return torch.rsqrt((v * v).mean(1, keepdim=True) + eps)
+
+
+NORMS = [(1, 8), (3, 9), (5, 17), (64, 64), (256, 479), (33, 512), (10, 351), (130, 1000),
+         (20, 1664), (700, 3328), (9, 4096), (6, 5003), (5, 8192), (2000, 40)]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("gate,sig", [("none", False), ("row", True), ("row", False),
+                                      ("element", True), ("element", False)])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("n,dim", NORMS)
+def test_gated_norm(n, dim, kind, gate, sig, post):
+    t, eps = TYPES[kind], 1e-6
+    x, block, gt, w_post, scale, w_pre, dy, dh = norm_inputs(n + dim, n, dim, t, gate, post)
+    code = gate_code(gate, sig)
+    y, c0 = guarded((n, dim), t, shift=1)
+    h, c1 = guarded((n, dim), t, shift=1)
+    eb.check(eb.emb_gated_norm_forward(x, block, gt, w_post, scale, w_pre, n, dim,
+                                       eb.dtype_code(t), code, eps, y, h), "forward")
+    torch.cuda.synchronize()
+    c0()
+    c1()
+    d, er = sum_steps(dim, t), (sum_steps(dim, t) / 2 + 4) * U
+    o = block.double()
+    ro = rms_inv(o, eps) if post else torch.ones(1, 1, dtype=torch.float64, device=DEV)
+    eo = er if post else 0.0
+    wp = w_post.double() if post else torch.ones(dim, dtype=torch.float64, device=DEV)
+    a, ea = gate_of(gt, sig)
+    ohat, sc, wn = o * ro, scale.double(), w_pre.double()
+    u = ohat * wp
+    br = sc * a * u
+    yr = x.double() + br
+    dY = br.abs() * (eo + ea + 5 * U) + U * yr.abs()
+    within(y, yr, dY, "y")
+    ry = rms_inv(yr, eps)
+    ery = er + (yr.abs() * dY).sum(1, keepdim=True) / ((yr * yr).sum(1, keepdim=True) + dim * eps)
+    hr = yr * ry * wn
+    within(h, hr, (ry * wn).abs() * dY + hr.abs() * (ery + 3 * U), "h")
+
+    # backward, from the stored y
+    outs = [guarded((n, dim), t, shift=1) for _ in range(2)]
+    (dx, c2), (db, c3) = outs
+    dg, c4 = (None, lambda: None) if gt is None else guarded(tuple(gt.shape), t, shift=1)
+    dwp, c5 = guarded((dim,), torch.float32) if post else (None, lambda: None)
+    dsc, c6 = guarded((dim,), torch.float32)
+    dwn, c7 = guarded((dim,), torch.float32)
+    need = eb.emb_gated_norm_workspace_bytes(n, dim)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV).fill_(255)
+    eb.check(eb.emb_gated_norm_backward(y, block, gt, w_post, scale, w_pre, dy, dh, n, dim,
+                                        eb.dtype_code(t), code, eps, dx, db, dg, dwp, dsc, dwn,
+                                        ws, need), "backward")
+    torch.cuda.synchronize()
+    for c in (c2, c3, c4, c5, c6, c7):
+        c()
+    yd, g, q = y.double(), dy.double(), dh.double() * wn
+    ry = rms_inv(yd, eps)
+    yhat = yd * ry
+    mq = (q * yhat).mean(1, keepdim=True)
+    dmq = (q * yhat).abs().mean(1, keepdim=True) * ((d + 2) * U + er + 2 * U)
+    tt = g + ry * (q - yhat * mq)
+    B = q.abs() + (yhat * mq).abs()
+    dT = ry * (4 * U * B + (yhat * mq).abs() * er + yhat.abs() * dmq) + er * ry * B + \
+        2 * U * (tt.abs() + g.abs())
+    within(dx, tt, dT, "dx")
+    p = tt * sc * a * wp
+    dP = (sc * a * wp).abs() * dT + p.abs() * (ea + 5 * U)
+    if post:
+        mp = (p * ohat).mean(1, keepdim=True)
+        dmp = (ohat.abs() * dP + (p * ohat).abs() * (eo + 4 * U)).mean(1, keepdim=True) + \
+            (d + 2) * U * (p * ohat).abs().mean(1, keepdim=True)
+        P = p.abs() + (ohat * mp).abs()
+        do = ro * (p - ohat * mp)
+        eD = ro * (dP + ohat.abs() * dmp + (ohat * mp).abs() * (eo + 3 * U)) + \
+            (eo + 4 * U) * ro * P
+    else:
+        do, eD = p, dP
+    within(db, do, eD, "dblock")
+    if gt is not None:
+        f = a * (1 - a) if sig else torch.ones_like(a)
+        df = f * (ea + 3 * U) + a * (a * ea + U) if sig else torch.zeros_like(a)
+        v, ev = tt * sc * u, (sc * u).abs() * dT + (tt * sc * u).abs() * (eo + 5 * U)
+        if gate == "row":
+            ev = ev.sum(1, keepdim=True) + d * U * v.abs().sum(1, keepdim=True)
+            v = v.sum(1, keepdim=True)
+        ref = (v * f).reshape(gt.shape)
+        within(dg, ref, (f * ev + v.abs() * df + 2 * U * (v * f).abs()).reshape(gt.shape), "dgate")
+    # a block's rows one after another, the row groups of a block, 512 blocks in 16 groups
+    steps = -(-n // 512) + 32 + 32 + 16
+    for got, terms, e, what in (
+            (dwp, tt * sc * a * ohat, (sc * a * ohat).abs() * dT, "dw_post"),
+            (dsc, tt * a * u, (a * u).abs() * dT, "dscale"),
+            (dwn, dh.double() * yhat, 0.0, "dw_pre")):
+        if got is not None:
+            e = e + terms.abs() * (ea + eo + er + 5 * U)
+            within(got, terms.sum(0), e.sum(0) + steps * U * terms.abs().sum(0), what)
+
+
+def test_gated_norm_gradients_against_differences():
+    """The backward's 32-bit gradients against central differences of the formula in 64 bits."""
+    n, dim, eps, step = 4, 12, 1e-6, 1e-6
+    x, block, gt, w_post, scale, w_pre, dy, dh = norm_inputs(2, n, dim, torch.float32, "element",
+                                                             True)
+
+    def value(x, block, gt, w_post, scale, w_pre):
+        u = block * rms_inv(block, eps) * w_post
+        y = x + scale * torch.sigmoid(gt) * u
+        return float((y * dy.double()).sum() + (y * rms_inv(y, eps) * w_pre * dh.double()).sum())
+
+    leaves = [v.double() for v in (x, block, gt, w_post, scale, w_pre)]
+    y, h = torch.empty(n, dim, device=DEV), torch.empty(n, dim, device=DEV)
+    code = gate_code("element", True)
+    eb.check(eb.emb_gated_norm_forward(x, block, gt, w_post, scale, w_pre, n, dim, 0, code, eps, y,
+                                       h), "forward")
+    got = [torch.empty(n, dim, device=DEV) for _ in range(3)] + \
+        [torch.empty(dim, device=DEV) for _ in range(3)]
+    need = eb.emb_gated_norm_workspace_bytes(n, dim)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    eb.check(eb.emb_gated_norm_backward(y, block, gt, w_post, scale, w_pre, dy, dh, n, dim, 0,
+                                        code, eps, *got, ws, need), "backward")
+    for which, (leaf, grad) in enumerate(zip(leaves, got)):
+        flat = leaf.reshape(-1)
+        for i in range(0, flat.numel(), 5):
+            keep = float(flat[i])
+            flat[i] = keep + step
+            up = value(*leaves)
+            flat[i] = keep - step
+            down = value(*leaves)
+            flat[i] = keep
+            # the difference's own error: curvature (step^2) and 64-bit cancellation
+            assert abs((up - down) / (2 * step) - float(grad.reshape(-1)[i])) < 2e-4, (which, i)
+
+
+def test_gated_norm_rows_do_not_touch_each_other():
+    for dim, n in ((24, 50), (200, 70), (3328, 9)):
+        x, block, gt, w_post, scale, w_pre, dy, dh = norm_inputs(7, n, dim, torch.bfloat16,
+                                                                 "element", True)
+
+        def run():
+            y, h = torch.empty_like(x), torch.empty_like(x)
+            eb.check(eb.emb_gated_norm_forward(x, block, gt, w_post, scale, w_pre, n, dim, 1,
+                                               gate_code("element", True), 1e-6, y, h), "forward")
+            torch.cuda.synchronize()
+            return y, h
+        y0, h0 = run()
+        x[3], block[5], gt[6], block[7] = float("nan"), float("inf"), float("-inf"), 0.0
+        y1, h1 = run()
+        rows = [r for r in range(n) if r not in (3, 5, 6, 7)]
+        assert torch.equal(y0[rows], y1[rows]) and torch.equal(h0[rows], h1[rows])
+        assert torch.isnan(y1[3]).all() and torch.isnan(h1[3]).all()
+        assert torch.equal(y1[6], x[6])  # a closed gate passes the residual
+        assert torch.equal(y1[7], x[7])  # as does a block of zeros
+        z = x.clone()                    # y over x, h elsewhere
+        h2 = torch.empty_like(x)
+        eb.check(eb.emb_gated_norm_forward(z, block, gt, w_post, scale, w_pre, n, dim, 1,
+                                           gate_code("element", True), 1e-6, z, h2), "in place")
+        torch.cuda.synchronize()
+        assert torch.equal(z[rows], y0[rows]) and torch.equal(h2[rows], h0[rows])
+
+
+def test_no_rows():
+    dim = 40
+    one = torch.ones(dim, device=DEV)
+    need = eb.emb_gated_norm_workspace_bytes(0, dim)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    outs = [torch.full((dim,), 3.0, device=DEV) for _ in range(3)]
+    eb.check(eb.emb_gated_norm_backward(None, None, None, one, one, one, None, None, 0, dim, 0, 0,
+                                        1e-6, None, None, None, *outs, ws, need), "backward")
+    torch.cuda.synchronize()
+    assert all((o == 0).all() for o in outs)
+
+
+# ---------------------------------------------------------------- streams and graphs
+
+def dense_step(s, stream=None):
+    n, k, e, dim, code = 96, 2, 8, 351, 1
+    chk = eb.check
+    chk(eb.emb_expert_sort(s["ids"], n, k, e, 0, s["off"], s["src"], s["pos"], s["ws"],
+                           s["ws"].numel(), stream), "sort")
+    a = (n, k, n * k, dim, code)
+    chk(eb.emb_expert_dispatch(s["x"], s["pos"], s["src"], *a, s["xs"], stream), "dispatch")
+    chk(eb.emb_expert_combine(s["xs"], s["pos"], s["w"], *a, s["blk"], stream), "combine")
+    chk(eb.emb_gated_norm_forward(s["x"], s["blk"], s["gate"], s["p"][0], s["p"][1], s["p"][2], n,
+                                  dim, code, eb.EMB_GATE_ROW | eb.EMB_GATE_SIGMOID, 1e-6, s["y"],
+                                  s["h"], stream), "norm")
+    chk(eb.emb_gated_norm_backward(s["y"], s["blk"], s["gate"], s["p"][0], s["p"][1], s["p"][2],
+                                   s["dy"], s["h"], n, dim, code,
+                                   eb.EMB_GATE_ROW | eb.EMB_GATE_SIGMOID, 1e-6, s["dx"], s["db"],
+                                   s["dg"], s["dp"][0], s["dp"][1], s["dp"][2], s["ws"],
+                                   s["ws"].numel(), stream), "norm backward")
+    chk(eb.emb_expert_combine_backward(s["db"], s["xs"], s["pos"], s["src"], s["w"], *a, s["dys"],
+                                       s["dw"], stream), "combine backward")
+    chk(eb.emb_expert_dispatch_backward(s["dys"], s["pos"], *a, s["dx2"], stream), "dispatch back")
+    chk(eb.emb_clip_grad_norm(s["in"], s["out"], None, 0, 0.5, s["norm"], s["ws"],
+                              s["ws"].numel(), stream), "clip")
+
+
+def dense_state():
+    g, n, k, e, dim, b = gen(11), 96, 2, 8, 351, torch.bfloat16
+    i32 = dict(dtype=torch.int32, device=DEV)
+    s = {"ids": t_(choices(4, n, k, e, 0.1)), "off": torch.zeros(e + 1, **i32),
+         "src": torch.zeros(n * k, **i32), "pos": torch.zeros(n, k, **i32),
+         "x": rand(g, n, dim).to(b), "w": torch.rand(n, k, generator=g, device=DEV),
+         "gate": rand(g, n).to(b), "p": [rand(g, dim) for _ in range(3)],
+         "dy": rand(g, n, dim).to(b), "dg": torch.zeros(n, dtype=b, device=DEV),
+         "dp": [torch.zeros(dim, device=DEV) for _ in range(3)],
+         "dw": torch.zeros(n, k, device=DEV), "norm": torch.zeros(2, device=DEV),
+         "ws": torch.zeros(8 << 20, dtype=torch.uint8, device=DEV)}
+    for v in ("blk", "y", "h", "dx", "db", "dx2"):
+        s[v] = torch.zeros(n, dim, dtype=b, device=DEV)
+    for v in ("xs", "dys"):
+        s[v] = torch.zeros(n * k, dim, dtype=b, device=DEV)
+    s["clipped"] = [torch.zeros_like(v) for v in s["dp"]] + [torch.zeros_like(s["dw"])]
+    s["in"], s["out"] = eb.TensorList(s["dp"] + [s["dw"]]), eb.TensorList(s["clipped"])
+    return s
+
+
+def results(s):
+    return [v.clone() for k, v in s.items() if isinstance(v, torch.Tensor) and k != "ws"] + \
+        [v.clone() for v in s["dp"] + s["clipped"]]
+
+
+def test_another_stream_and_a_graph_give_the_eager_bits():
+    ref = dense_state()
+    dense_step(ref)
+    torch.cuda.synchronize()
+    want = results(ref)
+    side, other = torch.cuda.Stream(), dense_state()
+    side.wait_stream(torch.cuda.current_stream())
+    dense_step(other, side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(results(other), want)), "another stream"
+    s = dense_state()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        dense_step(s, torch.cuda.current_stream())
+    for r in range(4):
+        for v in ("y", "h", "dx", "db", "xs", "dys"):
+            s[v].zero_()
+        graph.replay()
+        scratch = torch.randn(1 << 20, device=DEV).sum()  # eager work of the program
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(results(s), want)), f"replay {r}"
+        del scratch
