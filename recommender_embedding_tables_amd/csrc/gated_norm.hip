@@ -18,30 +18,64 @@
 //   dw_post = sum_rows du * ohat;  dscale = sum_rows t * a * u;
 //   dw_pre = sum_rows dh * yhat
 //
-// Bound by memory: each stream is read or written once.  A row's vectors live
-// in the registers of the threads that share it (lanes of one wave for short
-// rows, the whole block for long ones), so the statistics and the results come
-// from one read.  The blocks walk over rows and keep the weights of their
-// columns, and in the backward pass the columns' sums, in registers.  The sums
-// of a block go to the workspace and a second kernel adds them in block order:
-// no atomics, the result does not depend on timing.
+// Bound by memory: each stream is read or written once (a large device copy
+// reaches 5.2 TB/s here).  A row's vectors live in the registers of the threads
+// that share it (lanes of one wave for short rows, the whole block for long
+// ones), so the statistics and the results come from one read, and the loads
+// of a thread's next row are issued with the stores of this one.  Issuing them
+// a row ahead, into a second set of registers, left fewer waves and gained
+// nothing (32768 x 3328 bf16: 214 us against 210).  The blocks walk over rows
+// and keep the weights of their columns, and in the backward pass the columns'
+// sums.  The sums of a block go to the workspace and a second kernel adds them
+// in block order: no atomics, the result does not depend on timing.
+//
+// Element-wise sigmoid gate, norm before the gate:
+//   forward   32768 x 3328 bf16   210 us, 5.2 TB/s
+//   backward  16384 x 3328 bf16   187 us, 4.7 TB/s (its column sums 11 us of it)
+// What moved them there: sums by lane permutations in place of LDS shuffles,
+// the hardware's exponential and reciprocal for 16-bit gates, weights in LDS.
 #include "dense.hpp"
 
 namespace embtab {
 
 namespace {
 
-constexpr int kMaxBlocksForward = 2048;
-constexpr int kMaxBlocksBackward = 512;
-constexpr int kMaxWaves = 16;
+typedef float fv4 __attribute__((ext_vector_type(4)));
 
-__device__ inline float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+constexpr int kMaxWaves = 16;
+// Waves a launch puts on each of the 256 CUs: few blocks that walk over many
+// rows each, so that the weights and column sums are set up once.  Measured on
+// 65536 x 512 bf16 rows: forward 61 us at 14 waves, 68 at 28; backward, whose
+// blocks leave 12 * dim bytes of sums each, 112 us at 8 waves, 122 at 16.  A
+// row that takes a whole block needs two blocks to hide its barriers (3328
+// columns: 7 waves each).
+constexpr int kCus = 256;
+constexpr int kForwardWaves = 14, kBackwardWaves = 8, kBackwardBlockRowWaves = 16;
+
+// 1 / (1 + 2^(-v log2 e)).  For 16-bit data the exponent is one product and the
+// quotient the hardware reciprocal (both within 2^-21 for |v| < 8, far below
+// the data's own rounding); infinite gates give 0 and 1, a NaN stays one.
+// fp32 takes the library's exponential.
+template <class T>
+__device__ inline float sigmoid(float v) {
+  if constexpr (sizeof(T) == 4) return 1.0f / (1.0f + expf(-v));
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896340736f));
+}
+
+// 1 / sqrt(x) by the hardware instruction (1 ulp), which takes no denormals:
+// those are scaled up by 2^64 first.
+__device__ inline float inv_sqrt(float x) {
+  const bool tiny = x < 0x1p-100f;
+  return __builtin_amdgcn_rsqf(tiny ? x * 0x1p64f : x) * (tiny ? 0x1p32f : 1.0f);
+}
 
 // How the rows lie on the threads: tpr threads share a row (8 .. 64 lanes of
-// a wave, or, MULTI, the whole block), each holding V vectors of it.
+// a wave, or, MULTI, the whole block), each holding V vectors of it, at most 8
+// values: the backward pass holds about 15 registers for each.
 struct Shape {
   int32_t tpr, threads, vecs, multi;
   int32_t rows_per_block() const { return multi ? 1 : threads / tpr; }
+  int32_t waves() const { return threads / 64; }
 };
 
 template <class T>
@@ -50,47 +84,80 @@ Shape shape_of(int32_t dim) {
   Shape s{8, 256, 1, 0};
   while (s.tpr < 64 && s.tpr < nvec) s.tpr *= 2;
   if (nvec <= 64) return s;
-  if (nvec <= 128) {
-    s.vecs = 2;
-    return s;
-  }
+  s.vecs = sizeof(T) == 4 ? 2 : 1;
+  if (nvec <= 64 * s.vecs) return s;
   s.multi = 1;
-  s.vecs = nvec <= 1024 ? 1 : 2;
   s.tpr = s.threads = ((nvec + s.vecs - 1) / s.vecs + 63) / 64 * 64;
   return s;
 }
 
-// Sums of N values over the threads of a row.  MULTI rows pass through LDS;
-// the caller alternates between two buffers, so one barrier per sum suffices.
-template <bool MULTI, int N>
-__device__ inline void row_sum(float (&v)[N], int tpr, float (*lds)[kMaxWaves]) {
-  if (MULTI) {
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) v[k] += __shfl_xor(v[k], o, 64);
-    const int waves = blockDim.x >> 6;
-    if ((threadIdx.x & 63u) == 0u)
-#pragma unroll
-      for (int k = 0; k < N; ++k) lds[k][threadIdx.x >> 6] = v[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      float t = 0.0f;
-      for (int w = 0; w < waves; ++w) t += lds[k][w];
-      v[k] = t;
-    }
-  } else {
-    for (int o = tpr >> 1; o > 0; o >>= 1)
-#pragma unroll
-      for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], o, 64);
-  }
+template <int CTRL>
+__device__ inline float dpp(float v) {
+  return __uint_as_float(
+      (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
 }
 
-// The columns of one thread: vector v starts at col[v]; elements before
-// skip[v] belong to the vector before it (the last vector of a row is moved
-// back to end with the row) or to none (skip = the vector's width).
-template <class T, int V>
+// Sum over groups of tpr (8, 16, 32 or 64) neighbouring lanes, in every lane:
+// quads, half rows and rows by lane permutations, then pairs of rows and the
+// halves of the wave by row swaps; no LDS.  Both lanes of a pair add the same
+// two values, so the lanes' results have the same bits.
+__device__ inline float lanes_sum(float v, int tpr) {
+  v += dpp<0xB1>(v);   // quad_perm 1,0,3,2
+  v += dpp<0x4E>(v);   // quad_perm 2,3,0,1
+  v += dpp<0x141>(v);  // the other quad of 8
+  if (tpr >= 16) v += dpp<0x140>(v);  // the other half of 16
+  if (tpr >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if (tpr >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
+}
+
+// Sums of N values over the threads of a row.  MULTI rows pass through LDS,
+// with one barrier: the calls of a kernel alternate between two buffers, so a
+// wave that writes for the next sum never meets one that still reads this
+// one.  Lane l then takes wave l % 16's part (zero for a wave the block does
+// not have) and the 16 are added as above.
+struct SumBuffers {
+  float part[2][3][kMaxWaves];
+};
+
+template <bool MULTI, int N>
+__device__ inline void row_sum(float (&v)[N], int tpr, SumBuffers& lds, uint32_t& turn) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = lanes_sum(v[k], MULTI ? 64 : tpr);
+  if (!MULTI) return;
+  float(*part)[kMaxWaves] = lds.part[turn];
+  turn ^= 1u;
+  if ((threadIdx.x & 63u) == 0u)
+#pragma unroll
+    for (int k = 0; k < N; ++k) part[k][threadIdx.x >> 6] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = lanes_sum(part[k][threadIdx.x % kMaxWaves], kMaxWaves);
+}
+
+template <bool MULTI>
+__device__ inline void clear_sums(SumBuffers& lds) {
+  if (!MULTI) return;
+  for (uint32_t i = threadIdx.x; i < 2u * 3u * kMaxWaves; i += blockDim.x)
+    (&lds.part[0][0][0])[i] = 0.0f;
+  __syncthreads();
+}
+
+// The columns of one thread: vector v starts at col[v].  A vector that would
+// pass the row's end is moved back to end with it (TAIL: the width is not a
+// multiple of the vector); its elements before skip[v] belong to the vector
+// before and are left out of sums, and stored twice with the same value.  A
+// vector past the row (skip = its width) repeats the last one and stores
+// nothing.
+template <class T, int V, bool TAIL>
 struct Columns {
   uint32_t col[V], skip[V];
   __device__ Columns(uint32_t lane, uint32_t tpr, uint32_t dim) {
@@ -102,336 +169,481 @@ struct Columns {
     }
   }
   __device__ bool any(int v) const { return skip[v] < kVec<T>; }
-  __device__ bool owns(int v, int e) const { return (uint32_t)e >= skip[v]; }
+  // of a vector with any(v)
+  __device__ bool owns(int v, int e) const { return !TAIL || (uint32_t)e >= skip[v]; }
+};
+
+// A thread's share of the fp32 weight vectors, 1 where the vector is null.  A
+// wave's rows keep it in registers; a block's rows (MULTI) in LDS, [value / 4]
+// [thread] in 16-byte steps without bank conflicts, each thread its own and so
+// without barriers: 24 registers less, without which the backward pass spills.
+template <class T, int V, bool MULTI>
+struct Weights {
+  float w[V][kVec<T>];
+  template <bool TAIL>
+  __device__ inline void load(const float* p, const Columns<T, V, TAIL>& c) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int e = 0; e < kVec<T>; e += 4) {
+        const Raw<float> r = p ? load_raw(p + c.col[v] + e) : Raw<float>{};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[v][e + i] = p ? r.get(i) : 1.0f;
+      }
+  }
+  __device__ inline fv4 get(int v, int e) const {  // values e .. e + 3 of vector v
+    return fv4{w[v][e], w[v][e + 1], w[v][e + 2], w[v][e + 3]};
+  }
 };
 
 template <class T, int V>
-__device__ inline void load_weights(const float* w, const Columns<T, V>& c,
-                                    float (&out)[V][kVec<T>]) {
+struct Weights<T, V, true> {
+  fv4* mine;
+  template <bool TAIL>
+  __device__ inline void load(const float* p, const Columns<T, V, TAIL>& c) {
+    Weights<T, V, false> r;
+    r.load(p, c);
 #pragma unroll
-  for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int e = 0; e < kVec<T>; ++e) out[v][e] = w ? w[c.col[v] + e] : 1.0f;
-}
+      for (int e = 0; e < kVec<T>; e += 4)
+        mine[(v * kVec<T> + e) / 4 * blockDim.x] =
+            fv4{r.w[v][e], r.w[v][e + 1], r.w[v][e + 2], r.w[v][e + 3]};
+  }
+  __device__ inline fv4 get(int v, int e) const {
+    return mine[(v * kVec<T> + e) / 4 * blockDim.x];
+  }
+};
 
 template <class T, int V, bool MULTI>
+__device__ inline void place_weights(Weights<T, V, MULTI> (&w)[3]) {
+  if constexpr (MULTI) {
+    extern __shared__ fv4 weights_lds[];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      w[k].mine = weights_lds + k * (V * kVec<T> / 4) * blockDim.x + threadIdx.x;
+  }
+}
+
+// One row's vectors of S streams, and its gate value for a row gate.
+template <class T, int V, int S>
+struct RowData {
+  Raw<T> in[S][V], gate[V];
+  float a;
+
+  template <bool TAIL>
+  __device__ inline void load(const T* const (&p)[S], const T* g, int32_t gate_kind, int64_t r,
+                              uint32_t dim, const Columns<T, V, TAIL>& c) {
+    const size_t at = (size_t)r * dim;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) in[s][v] = load_raw<T, kVec<T>, true>(p[s] + at + c.col[v]);
+      if (gate_kind == EMB_GATE_ELEMENT)
+        gate[v] = load_raw<T, kVec<T>, true>(g + at + c.col[v]);
+    }
+    a = gate_kind == EMB_GATE_ROW ? to_f32(g[r]) : 1.0f;
+  }
+
+  // The gate's factors; a becomes the row's.
+  __device__ inline void factors(int32_t gate_kind, bool sig, float (&out)[V][kVec<T>]) {
+    if (gate_kind == EMB_GATE_ELEMENT) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e)
+          out[v][e] = sig ? sigmoid<T>(gate[v].get(e)) : gate[v].get(e);
+    } else {
+      if (sig) a = sigmoid<T>(a);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e) out[v][e] = a;
+    }
+  }
+};
+
+enum { kPost = 0, kScale = 1, kPre = 2 };  // the weight vectors
+
+template <class T, int V, bool MULTI, bool TAIL>
 __global__ __launch_bounds__(MULTI ? 1024 : 256) void k_gated_norm_forward(
     const T* x, const T* block, const T* gate, const float* __restrict__ w_post,
     const float* __restrict__ scale, const float* __restrict__ w_pre, int64_t rows, uint32_t dim,
     int32_t tpr, int32_t gate_kind, bool sig, float eps, T* y, T* h) {
   constexpr int N = kVec<T>;
-  __shared__ float lds[2][1][kMaxWaves];
+  __shared__ SumBuffers lds;
+  uint32_t turn = 0;
   const uint32_t lane = MULTI ? threadIdx.x : threadIdx.x % (uint32_t)tpr;
   const uint32_t rpb = MULTI ? 1u : blockDim.x / (uint32_t)tpr;
-  const Columns<T, V> c(lane, (uint32_t)tpr, dim);
+  const uint32_t mine = MULTI ? 0u : threadIdx.x / (uint32_t)tpr;
+  const Columns<T, V, TAIL> c(lane, (uint32_t)tpr, dim);
   const float inv = 1.0f / (float)dim;
-  float wpost[V][N], sc[V][N], wpre[V][N];
-  load_weights<T, V>(w_post, c, wpost);
-  load_weights<T, V>(scale, c, sc);
-  load_weights<T, V>(w_pre, c, wpre);
-  const int64_t step = (int64_t)gridDim.x * rpb;
+  const T* const in[2] = {x, block};
+  const int64_t step = (int64_t)gridDim.x * rpb, last = rows - 1;
+  RowData<T, V, 2> cur;
+  int64_t r = (int64_t)blockIdx.x * rpb + mine;
+  cur.load(in, gate, gate_kind, r < last ? r : last, dim, c);
+  Weights<T, V, MULTI> w[3];
+  place_weights<T, V, MULTI>(w);
+  w[kPost].load(w_post, c);
+  w[kScale].load(scale, c);
+  w[kPre].load(w_pre, c);
+  clear_sums<MULTI>(lds);
   // every thread of a block takes the same number of rounds (barriers)
-  for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < rows; r0 += step) {
-    const int64_t r = MULTI ? r0 : r0 + threadIdx.x / (uint32_t)tpr;
-    const bool live = r < rows;
-    const size_t at = (size_t)(live ? r : rows - 1) * dim;
-    Raw<T> rx[V], ro[V], rg[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      ro[v] = load_raw<T, N, true>(block + at + c.col[v]);
-      rx[v] = load_raw<T, N, true>(x + at + c.col[v]);
-      if (gate_kind == EMB_GATE_ELEMENT) rg[v] = load_raw<T, N, true>(gate + at + c.col[v]);
-    }
-    float a_row = 1.0f;
-    if (gate_kind == EMB_GATE_ROW) {
-      a_row = to_f32(gate[live ? r : rows - 1]);
-      if (sig) a_row = sigmoid(a_row);
-    }
+  for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < rows; r0 += step, r += step) {
+    float a[V][N];
+    cur.factors(gate_kind, sig, a);
     float ro_s = 1.0f;
     if (w_post) {
       float s[1] = {0.0f};
 #pragma unroll
       for (int v = 0; v < V; ++v)
+        if (c.any(v))
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float o = c.owns(v, e) ? ro[v].get(e) : 0.0f;
-          s[0] = __builtin_fmaf(o, o, s[0]);
-        }
-      row_sum<MULTI, 1>(s, tpr, lds[0]);
-      ro_s = 1.0f / sqrtf(s[0] * inv + eps);
+          for (int e = 0; e < N; ++e) {
+            const float o = c.owns(v, e) ? cur.in[1][v].get(e) : 0.0f;
+            s[0] = __builtin_fmaf(o, o, s[0]);
+          }
+      row_sum<MULTI, 1>(s, tpr, lds, turn);
+      ro_s = inv_sqrt(s[0] * inv + eps);
     }
     float yv[V][N];
     float s[1] = {0.0f};
 #pragma unroll
     for (int v = 0; v < V; ++v)
+      if (c.any(v))
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        float a = a_row;
-        if (gate_kind == EMB_GATE_ELEMENT) a = sig ? sigmoid(rg[v].get(e)) : rg[v].get(e);
-        const float u = (ro[v].get(e) * ro_s) * wpost[v][e];
-        yv[v][e] = __builtin_fmaf(sc[v][e] * a, u, rx[v].get(e));
-        const float t = c.owns(v, e) ? yv[v][e] : 0.0f;
-        s[0] = __builtin_fmaf(t, t, s[0]);
+        for (int e0 = 0; e0 < N; e0 += 4) {
+          const fv4 wpost = w[kPost].get(v, e0), sc = w[kScale].get(v, e0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int e = e0 + i;
+            const float u = (cur.in[1][v].get(e) * ro_s) * wpost[i];
+            yv[v][e] = __builtin_fmaf(sc[i] * a[v][e], u, cur.in[0][v].get(e));
+            const float t = c.owns(v, e) ? yv[v][e] : 0.0f;
+            s[0] = __builtin_fmaf(t, t, s[0]);
+          }
+        }
+    row_sum<MULTI, 1>(s, tpr, lds, turn);
+    const float ry = inv_sqrt(s[0] * inv + eps);
+    if (r < rows) {
+      const size_t at = (size_t)r * dim;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (!c.any(v)) continue;
+        Raw<T> o;
+        o.set_all(yv[v]);
+        store_raw<T, N, true>(y + at + c.col[v], o);
+        float hv[N];
+#pragma unroll
+        for (int e0 = 0; e0 < N; e0 += 4) {
+          const fv4 wpre = w[kPre].get(v, e0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) hv[e0 + i] = (yv[v][e0 + i] * ry) * wpre[i];
+        }
+        o.set_all(hv);
+        store_raw<T, N, true>(h + at + c.col[v], o);
       }
-    row_sum<MULTI, 1>(s, tpr, lds[1]);
-    const float ry = 1.0f / sqrtf(s[0] * inv + eps);
-    // Without w_post a MULTI round has one barrier: the next round must not
-    // write lds[1] while a slower wave still reads it.
-    if (MULTI && !w_post) __syncthreads();
-    if (!live) continue;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (!c.any(v)) continue;
-      Raw<T> o;
-      o.set_all(yv[v]);
-      store_raw<T, N, true>(y + at + c.col[v], o);
-      float hv[N];
-#pragma unroll
-      for (int e = 0; e < N; ++e) hv[e] = (yv[v][e] * ry) * wpre[v][e];
-      o.set_all(hv);
-      store_raw<T, N, true>(h + at + c.col[v], o);
     }
+    if (r0 + step < rows)
+      cur.load(in, gate, gate_kind, r + step < last ? r + step : last, dim, c);
   }
 }
 
-template <class T, int V, bool MULTI>
+template <class T, int V, bool MULTI, bool TAIL>
 __global__ __launch_bounds__(MULTI ? 1024 : 256) void k_gated_norm_backward(
     const T* y, const T* block, const T* gate, const float* __restrict__ w_post,
     const float* __restrict__ scale, const float* __restrict__ w_pre, const T* dy, const T* dh,
     int64_t rows, uint32_t dim, int32_t tpr, int32_t gate_kind, bool sig, float eps, T* dx,
     T* dblock, T* dgate, float* __restrict__ parts) {
   constexpr int N = kVec<T>;
-  __shared__ float lds[2][3][kMaxWaves];
+  enum { Y = 0, O = 1, DH = 2, DY = 3 };
+  __shared__ SumBuffers lds;
+  uint32_t turn = 0;
   const uint32_t lane = MULTI ? threadIdx.x : threadIdx.x % (uint32_t)tpr;
   const uint32_t rpb = MULTI ? 1u : blockDim.x / (uint32_t)tpr;
-  const Columns<T, V> c(lane, (uint32_t)tpr, dim);
+  const uint32_t mine = MULTI ? 0u : threadIdx.x / (uint32_t)tpr;
+  const Columns<T, V, TAIL> c(lane, (uint32_t)tpr, dim);
   const float inv = 1.0f / (float)dim;
-  float wpost[V][N], sc[V][N], wpre[V][N];
-  load_weights<T, V>(w_post, c, wpost);
-  load_weights<T, V>(scale, c, sc);
-  load_weights<T, V>(w_pre, c, wpre);
+  const T* const in[4] = {y, block, dh, dy};
+  const int64_t step = (int64_t)gridDim.x * rpb, last = rows - 1;
+  RowData<T, V, 4> cur;
+  int64_t r = (int64_t)blockIdx.x * rpb + mine;
+  cur.load(in, gate, gate_kind, r < last ? r : last, dim, c);
+  Weights<T, V, MULTI> w[3];
+  place_weights<T, V, MULTI>(w);
+  w[kPost].load(w_post, c);
+  w[kScale].load(scale, c);
+  w[kPre].load(w_pre, c);
   float s_post[V][N], s_scale[V][N], s_pre[V][N];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int e = 0; e < N; ++e) s_post[v][e] = s_scale[v][e] = s_pre[v][e] = 0.0f;
-  const int64_t step = (int64_t)gridDim.x * rpb;
-  for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < rows; r0 += step) {
-    const int64_t r = MULTI ? r0 : r0 + threadIdx.x / (uint32_t)tpr;
+  clear_sums<MULTI>(lds);
+  for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < rows; r0 += step, r += step) {
     const bool live = r < rows;
-    const size_t at = (size_t)(live ? r : rows - 1) * dim;
-    Raw<T> ry_[V], ro[V], rg[V], rdy[V], rdh[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      ry_[v] = load_raw<T, N, true>(y + at + c.col[v]);
-      ro[v] = load_raw<T, N, true>(block + at + c.col[v]);
-      rdh[v] = load_raw<T, N, true>(dh + at + c.col[v]);
-      rdy[v] = load_raw<T, N, true>(dy + at + c.col[v]);
-      if (gate_kind == EMB_GATE_ELEMENT) rg[v] = load_raw<T, N, true>(gate + at + c.col[v]);
-    }
-    float a_row = 1.0f;
-    if (gate_kind == EMB_GATE_ROW) {
-      a_row = to_f32(gate[live ? r : rows - 1]);
-      if (sig) a_row = sigmoid(a_row);
-    }
+    float a[V][N];
+    cur.factors(gate_kind, sig, a);
     // sums of y^2, q * y and o^2
     float s1[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int v = 0; v < V; ++v)
+      if (c.any(v))
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const bool own = c.owns(v, e);
-        const float yy = own ? ry_[v].get(e) : 0.0f, o = own ? ro[v].get(e) : 0.0f;
-        s1[0] = __builtin_fmaf(yy, yy, s1[0]);
-        s1[1] = __builtin_fmaf(rdh[v].get(e) * wpre[v][e], yy, s1[1]);
-        s1[2] = __builtin_fmaf(o, o, s1[2]);
-      }
-    row_sum<MULTI, 3>(s1, tpr, lds[0]);
-    const float ry = 1.0f / sqrtf(s1[0] * inv + eps);
+        for (int e0 = 0; e0 < N; e0 += 4) {
+          const fv4 wpre = w[kPre].get(v, e0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int e = e0 + i;
+            const bool own = c.owns(v, e);
+            const float yy = cur.in[Y][v].get(e), o = cur.in[O][v].get(e);
+            const float q = cur.in[DH][v].get(e) * wpre[i];
+            s1[0] = own ? __builtin_fmaf(yy, yy, s1[0]) : s1[0];
+            s1[1] = own ? __builtin_fmaf(q, yy, s1[1]) : s1[1];
+            s1[2] = own ? __builtin_fmaf(o, o, s1[2]) : s1[2];
+          }
+        }
+    row_sum<MULTI, 3>(s1, tpr, lds, turn);
+    const float ry = inv_sqrt(s1[0] * inv + eps);
     const float mq = (s1[1] * ry) * inv;  // mean(q * yhat)
-    const float ro_s = w_post ? 1.0f / sqrtf(s1[2] * inv + eps) : 1.0f;
+    const float ro_s = w_post ? inv_sqrt(s1[2] * inv + eps) : 1.0f;
     // t, and the sums of p * ohat and t * scale * u over the row
     float s2[2] = {0.0f, 0.0f};
     float tv[V][N];
 #pragma unroll
     for (int v = 0; v < V; ++v)
+      if (c.any(v) && live)
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const bool own = live && c.owns(v, e);
-        const float yhat = ry_[v].get(e) * ry, dhv = rdh[v].get(e);
-        const float t = __builtin_fmaf(ry, dhv * wpre[v][e] - yhat * mq, rdy[v].get(e));
-        float a = a_row;
-        if (gate_kind == EMB_GATE_ELEMENT) a = sig ? sigmoid(rg[v].get(e)) : rg[v].get(e);
-        const float ohat = ro[v].get(e) * ro_s, u = ohat * wpost[v][e];
-        const float ts = t * sc[v][e];
-        tv[v][e] = t;
-        if (own) {
-          s2[0] = __builtin_fmaf(ts * a, u, s2[0]);
-          s2[1] = __builtin_fmaf(ts, u, s2[1]);
-          s_post[v][e] = __builtin_fmaf(ts * a, ohat, s_post[v][e]);
-          s_scale[v][e] = __builtin_fmaf(t * a, u, s_scale[v][e]);
-          s_pre[v][e] = __builtin_fmaf(dhv, yhat, s_pre[v][e]);
+        for (int e0 = 0; e0 < N; e0 += 4) {
+          const fv4 wpost = w[kPost].get(v, e0), sc = w[kScale].get(v, e0),
+                    wpre = w[kPre].get(v, e0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int e = e0 + i;
+            const float yhat = cur.in[Y][v].get(e) * ry, dhv = cur.in[DH][v].get(e);
+            const float t =
+                __builtin_fmaf(ry, dhv * wpre[i] - yhat * mq, cur.in[DY][v].get(e));
+            const float ohat = cur.in[O][v].get(e) * ro_s, u = ohat * wpost[i];
+            const float ts = t * sc[i];
+            tv[v][e] = t;
+            if (c.owns(v, e)) {
+              s2[0] = __builtin_fmaf(ts * a[v][e], u, s2[0]);
+              s2[1] = __builtin_fmaf(ts, u, s2[1]);
+              s_post[v][e] = __builtin_fmaf(ts * a[v][e], ohat, s_post[v][e]);
+              s_scale[v][e] = __builtin_fmaf(t * a[v][e], u, s_scale[v][e]);
+              s_pre[v][e] = __builtin_fmaf(dhv, yhat, s_pre[v][e]);
+            }
+          }
+        }
+    row_sum<MULTI, 2>(s2, tpr, lds, turn);
+    const float mp = s2[0] * inv;  // mean(p * ohat)
+    if (live) {
+      const size_t at = (size_t)r * dim;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (!c.any(v)) continue;
+        Raw<T> o;
+        o.set_all(tv[v]);
+        store_raw<T, N, true>(dx + at + c.col[v], o);
+        float ov[N], gv[N];
+#pragma unroll
+        for (int e0 = 0; e0 < N; e0 += 4) {
+          const fv4 wpost = w[kPost].get(v, e0), sc = w[kScale].get(v, e0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int e = e0 + i;
+            const float ohat = cur.in[O][v].get(e) * ro_s, ts = tv[v][e] * sc[i];
+            const float p = (ts * a[v][e]) * wpost[i], da = ts * (ohat * wpost[i]);
+            ov[e] = w_post ? ro_s * (p - ohat * mp) : p;
+            gv[e] = sig ? da * (a[v][e] * (1.0f - a[v][e])) : da;
+          }
+        }
+        o.set_all(ov);
+        store_raw<T, N, true>(dblock + at + c.col[v], o);
+        if (gate_kind == EMB_GATE_ELEMENT) {
+          o.set_all(gv);
+          store_raw<T, N, true>(dgate + at + c.col[v], o);
         }
       }
-    row_sum<MULTI, 2>(s2, tpr, lds[1]);
-    const float mp = s2[0] * inv;  // mean(p * ohat)
-    if (!live) continue;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (!c.any(v)) continue;
-      float o1[N], o2[N], o3[N];
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float t = tv[v][e];
-        float a = a_row;
-        if (gate_kind == EMB_GATE_ELEMENT) a = sig ? sigmoid(rg[v].get(e)) : rg[v].get(e);
-        const float ohat = ro[v].get(e) * ro_s, u = ohat * wpost[v][e];
-        const float ts = t * sc[v][e];
-        const float p = (ts * a) * wpost[v][e];
-        o1[e] = t;
-        o2[e] = w_post ? ro_s * (p - ohat * mp) : p;
-        o3[e] = sig ? (ts * u) * (a * (1.0f - a)) : ts * u;
-      }
-      Raw<T> o;
-      o.set_all(o1);
-      store_raw<T, N, true>(dx + at + c.col[v], o);
-      o.set_all(o2);
-      store_raw<T, N, true>(dblock + at + c.col[v], o);
-      if (gate_kind == EMB_GATE_ELEMENT) {
-        o.set_all(o3);
-        store_raw<T, N, true>(dgate + at + c.col[v], o);
-      }
+      if (gate_kind == EMB_GATE_ROW && lane == 0)
+        dgate[r] = from_f32<T>(sig ? s2[1] * (cur.a * (1.0f - cur.a)) : s2[1]);
     }
-    if (gate_kind == EMB_GATE_ROW && lane == 0)
-      dgate[r] = from_f32<T>(sig ? s2[1] * (a_row * (1.0f - a_row)) : s2[1]);
+    if (r0 + step < rows)
+      cur.load(in, gate, gate_kind, r + step < last ? r + step : last, dim, c);
   }
   // the block's column sums: [3][dim] of this block
   float* out = parts + (size_t)blockIdx.x * 3u * dim;
   if (MULTI) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
+      if (c.any(v))
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (c.owns(v, e)) {
-          out[c.col[v] + e] = s_post[v][e];
-          out[dim + c.col[v] + e] = s_scale[v][e];
-          out[2u * dim + c.col[v] + e] = s_pre[v][e];
-        }
+        for (int e = 0; e < N; ++e)
+          if (c.owns(v, e)) {
+            out[c.col[v] + e] = s_post[v][e];
+            out[dim + c.col[v] + e] = s_scale[v][e];
+            out[2u * dim + c.col[v] + e] = s_pre[v][e];
+          }
   } else {
-    // the block's row groups hold sums of the same columns: added through LDS
-    __shared__ float acc[256 * V * N];
+    // the block's row groups hold sums of the same columns: added through LDS,
+    // in the order of the groups
+    __shared__ float acc[3][V * N][256];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      float(&s)[V][N] = k == 0 ? s_post : k == 1 ? s_scale : s_pre;
-      __syncthreads();
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int e = 0; e < N; ++e)  // [group][v][e][lane]
-          acc[(((threadIdx.x / (uint32_t)tpr) * V + v) * N + e) * (uint32_t)tpr + lane] = s[v][e];
-      __syncthreads();
-      if (threadIdx.x < (uint32_t)tpr) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-          for (int e = 0; e < N; ++e)
-            if (c.owns(v, e)) {
-              float t = 0.0f;
-              for (uint32_t g = 0; g < rpb; ++g)
-                t += acc[((g * V + v) * N + e) * (uint32_t)tpr + lane];
-              out[(uint32_t)k * dim + c.col[v] + e] = t;
-            }
+      for (int e = 0; e < N; ++e) {
+        acc[0][v * N + e][threadIdx.x] = s_post[v][e];
+        acc[1][v * N + e][threadIdx.x] = s_scale[v][e];
+        acc[2][v * N + e][threadIdx.x] = s_pre[v][e];
       }
+    __syncthreads();
+    // one group of threads per sum: 256 / tpr groups take the 3 * V * N in turn
+    for (uint32_t k = mine; k < 3u * V * N; k += rpb) {
+      const uint32_t which = k / (V * N), ve = k % (V * N), v = ve / N, e = ve % N;
+      const uint32_t at = (lane + v * (uint32_t)tpr) * N;
+      if (at >= dim) continue;
+      const uint32_t col = at + N <= dim ? at : dim - N;
+      if (col + e < at) continue;
+      float t = 0.0f;
+      for (uint32_t g = 0; g < rpb; ++g) t += acc[which][ve][g * (uint32_t)tpr + lane];
+      out[which * dim + col + e] = t;
     }
   }
 }
 
-// dst[c] = sum over the blocks of parts[block][c], in block order per group of
-// blocks and then over the groups; 64 columns per block, 16 groups.
-constexpr int kSumGroups = 16;
-__global__ __launch_bounds__(64 * kSumGroups) void k_gated_norm_column_sums(
+// dst[c] = sum over the blocks of parts[block][c]: 32 columns per block, 32
+// groups of threads that take every 32nd part, eight loads in flight each, and
+// the groups in order.
+constexpr int kSumCols = 32, kSumGroups = 32, kSumAhead = 8;
+__global__ __launch_bounds__(kSumCols* kSumGroups) void k_gated_norm_column_sums(
     const float* __restrict__ parts, uint32_t blocks, uint32_t dim, float* __restrict__ dw_post,
     float* __restrict__ dscale, float* __restrict__ dw_pre) {
-  __shared__ float lds[kSumGroups][64];
-  const uint32_t col = blockIdx.x * 64u + (threadIdx.x & 63u), g = threadIdx.x >> 6;
-  const uint32_t width = 3u * dim;
+  __shared__ float lds[kSumGroups][kSumCols];
+  const uint32_t lane = threadIdx.x % kSumCols, g = threadIdx.x / kSumCols;
+  const uint32_t col = blockIdx.x * kSumCols + lane, width = 3u * dim;
   float s = 0.0f;
   if (col < width)
-    for (uint32_t b = g; b < blocks; b += kSumGroups) s += parts[(size_t)b * width + col];
-  lds[g][threadIdx.x & 63u] = s;
+    for (uint32_t b = g; b < blocks; b += kSumGroups * kSumAhead) {
+      float v[kSumAhead];
+#pragma unroll
+      for (int i = 0; i < kSumAhead; ++i) {
+        const uint32_t at = b + i * kSumGroups;
+        v[i] = at < blocks ? parts[(size_t)at * width + col] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kSumAhead; ++i) s += v[i];
+    }
+  lds[g][lane] = s;
   __syncthreads();
   if (g != 0 || col >= width) return;
   float t = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kSumGroups; ++i) t += lds[i][threadIdx.x];
+  for (int i = 0; i < kSumGroups; ++i) t += lds[i][lane];
   const uint32_t k = col / dim, j = col - k * dim;
   float* dst = k == 0 ? dw_post : k == 1 ? dscale : dw_pre;
   if (dst) dst[j] = t;
 }
 
-unsigned grid_of(int64_t rows, int32_t rpb, int most) {
-  const int64_t g = (rows + rpb - 1) / rpb;
+int backward_waves(const Shape& s) {
+  return s.multi ? kBackwardBlockRowWaves : kBackwardWaves;
+}
+
+unsigned grid_of(int64_t rows, const Shape& s, int waves_per_cu) {
+  const int64_t g = (rows + s.rows_per_block() - 1) / s.rows_per_block();
+  const int per_cu = waves_per_cu / s.waves() > 1 ? waves_per_cu / s.waves() : 1;
+  const int64_t most = (int64_t)kCus * per_cu;
   return (unsigned)(g < most ? g : most);
 }
+
+// Launch of KERNEL on a shape; a block's rows keep their weights in dynamic
+// LDS, which passes the default limit of 64 KB beyond 682 threads.
+template <class T, class Kernel, class... Args>
+hipError_t launch_rows(Kernel kernel, const Shape& sh, unsigned blocks, hipStream_t s,
+                       Args... args) {
+  const size_t lds = sh.multi ? (size_t)sh.vecs * kVec<T> * 12u * sh.threads : 0u;
+  if (lds > 64u * 1024u) {
+    const hipError_t e =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kernel, dim3(blocks), dim3((unsigned)sh.threads), lds, s, args...);
+  return hipGetLastError();
+}
+
+// CALL(V, MULTI, TAIL) of a shape.
+#define EMBTAB_GN_TAIL(V_, M_, CALL)             \
+  do {                                           \
+    if (a.dim % kVec<T>) return CALL(V_, M_, true); \
+    return CALL(V_, M_, false);                  \
+  } while (0)
+#define EMBTAB_GN_SHAPE(CALL)                              \
+  do {                                                     \
+    constexpr int kV = sizeof(T) == 4 ? 2 : 1;             \
+    if (sh.multi) EMBTAB_GN_TAIL(kV, true, CALL);          \
+    if (sh.vecs == kV) EMBTAB_GN_TAIL(kV, false, CALL);    \
+    EMBTAB_GN_TAIL(1, false, CALL);                        \
+  } while (0)
 
 template <class T>
 hipError_t forward_t(const GatedNorm& a, void* y, void* h, hipStream_t s) {
   const Shape sh = shape_of<T>(a.dim);
-  const dim3 grid(grid_of(a.rows, sh.rows_per_block(), kMaxBlocksForward)),
-      threads((unsigned)sh.threads);
-#define EMBTAB_GN(V_, M_)                                                                       \
-  hipLaunchKernelGGL((k_gated_norm_forward<T, V_, M_>), grid, threads, 0, s,                    \
-                     static_cast<const T*>(a.x), static_cast<const T*>(a.block),                \
-                     static_cast<const T*>(a.gate), a.w_post, a.scale, a.w_pre, a.rows,         \
-                     (uint32_t)a.dim, sh.tpr, a.gate_kind, a.sigmoid, a.eps, static_cast<T*>(y), \
-                     static_cast<T*>(h))
-  if (sh.multi) {
-    if (sh.vecs == 1) EMBTAB_GN(1, true);
-    else EMBTAB_GN(2, true);
-  } else {
-    if (sh.vecs == 1) EMBTAB_GN(1, false);
-    else EMBTAB_GN(2, false);
-  }
+  const unsigned blocks = grid_of(a.rows, sh, kForwardWaves);
+#define EMBTAB_GN(V_, M_, TAIL_)                                                                 \
+  launch_rows<T>(k_gated_norm_forward<T, V_, M_, TAIL_>, sh, blocks, s,                          \
+                 static_cast<const T*>(a.x), static_cast<const T*>(a.block),                     \
+                 static_cast<const T*>(a.gate), a.w_post, a.scale, a.w_pre, a.rows,              \
+                 (uint32_t)a.dim, sh.tpr, a.gate_kind, a.sigmoid, a.eps, static_cast<T*>(y),     \
+                 static_cast<T*>(h))
+  EMBTAB_GN_SHAPE(EMBTAB_GN);
 #undef EMBTAB_GN
-  return hipGetLastError();
 }
+
+template <class T>
+hipError_t backward_rows(const GatedNorm& a, const Shape& sh, unsigned blocks, const void* dy,
+                         const void* dh, void* dx, void* dblock, void* dgate, float* parts,
+                         hipStream_t s) {
+#define EMBTAB_GN(V_, M_, TAIL_)                                                                 \
+  launch_rows<T>(k_gated_norm_backward<T, V_, M_, TAIL_>, sh, blocks, s,                         \
+                 static_cast<const T*>(a.x), static_cast<const T*>(a.block),                     \
+                 static_cast<const T*>(a.gate), a.w_post, a.scale, a.w_pre,                      \
+                 static_cast<const T*>(dy), static_cast<const T*>(dh), a.rows, (uint32_t)a.dim,  \
+                 sh.tpr, a.gate_kind, a.sigmoid, a.eps, static_cast<T*>(dx),                     \
+                 static_cast<T*>(dblock), static_cast<T*>(dgate), parts)
+  EMBTAB_GN_SHAPE(EMBTAB_GN);
+#undef EMBTAB_GN
+}
+#undef EMBTAB_GN_SHAPE
+#undef EMBTAB_GN_TAIL
 
 template <class T>
 hipError_t backward_t(const GatedNorm& a, const void* dy, const void* dh, void* dx, void* dblock,
                       void* dgate, float* dw_post, float* dscale, float* dw_pre, float* parts,
                       hipStream_t s) {
   const Shape sh = shape_of<T>(a.dim);
-  const unsigned blocks = grid_of(a.rows, sh.rows_per_block(), kMaxBlocksBackward);
-  const dim3 grid(blocks), threads((unsigned)sh.threads);
-#define EMBTAB_GN(V_, M_)                                                                        \
-  hipLaunchKernelGGL((k_gated_norm_backward<T, V_, M_>), grid, threads, 0, s,                    \
-                     static_cast<const T*>(a.x), static_cast<const T*>(a.block),                 \
-                     static_cast<const T*>(a.gate), a.w_post, a.scale, a.w_pre,                  \
-                     static_cast<const T*>(dy), static_cast<const T*>(dh), a.rows,               \
-                     (uint32_t)a.dim, sh.tpr, a.gate_kind, a.sigmoid, a.eps,                     \
-                     static_cast<T*>(dx), static_cast<T*>(dblock), static_cast<T*>(dgate), parts)
+  const unsigned blocks = grid_of(a.rows, sh, backward_waves(sh));
   if (blocks) {
-    if (sh.multi) {
-      if (sh.vecs == 1) EMBTAB_GN(1, true);
-      else EMBTAB_GN(2, true);
-    } else {
-      if (sh.vecs == 1) EMBTAB_GN(1, false);
-      else EMBTAB_GN(2, false);
-    }
+    const hipError_t e =
+        backward_rows<T>(a, sh, blocks, dy, dh, dx, dblock, dgate, parts, s);
+    if (e != hipSuccess) return e;
   }
-#undef EMBTAB_GN
   const uint32_t width = 3u * (uint32_t)a.dim;
-  hipLaunchKernelGGL(k_gated_norm_column_sums, dim3((width + 63u) / 64u), dim3(64 * kSumGroups),
-                     0, s, parts, blocks, (uint32_t)a.dim, dw_post, dscale, dw_pre);
+  hipLaunchKernelGGL(k_gated_norm_column_sums, dim3((width + kSumCols - 1) / kSumCols),
+                     dim3(kSumCols * kSumGroups), 0, s, parts, blocks, (uint32_t)a.dim, dw_post,
+                     dscale, dw_pre);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// One [3][dim] fp32 part per block of the backward kernel.
+// One [3][dim] fp32 part per block of the backward kernel, of whichever type
+// takes more blocks.
 size_t gated_norm_workspace_bytes(int64_t rows, int32_t dim) {
-  const int64_t blocks = rows < kMaxBlocksBackward ? rows : kMaxBlocksBackward;
-  return (sizeof(float) * 3u * (size_t)dim * (size_t)blocks + 256) & ~(size_t)255;
+  const Shape wide = shape_of<float>(dim), narrow = shape_of<bf16_t>(dim);
+  const size_t a = grid_of(rows, wide, backward_waves(wide));
+  const size_t b = grid_of(rows, narrow, backward_waves(narrow));
+  return (sizeof(float) * 3u * (size_t)dim * (a > b ? a : b) + 256) & ~(size_t)255;
 }
 
 hipError_t launch_gated_norm_forward(const GatedNorm& a, int32_t dtype, void* y, void* h,
