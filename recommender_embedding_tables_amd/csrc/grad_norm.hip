@@ -24,30 +24,37 @@ namespace {
 
 constexpr int kClipThreads = 256;
 constexpr int kClipChunk = 8192;
-constexpr int kClipItems = 120;     // 32 bytes each: the table stays under 4 KiB
+constexpr int kClipItems = 104;     // 36 bytes each: the arguments stay under 4 KiB
 constexpr int kClipParts = 1024;    // blocks (and partial sums) of one sum launch
+constexpr int kScaleBlocks = 2048;  // blocks of one scale launch: what the chip holds
 
 struct ClipItem {
   const void* in;
   void* out;
   int64_t n;
-  uint32_t first;  // chunks of the items before
   uint32_t types;  // input type | output type << 8
 };
 struct ClipList {
   ClipItem item[kClipItems];
+  uint32_t first[kClipItems];  // chunks of the items before
   uint32_t count, chunks;
 };
+static_assert(kClipItems <= 128, "two per lane");
 
-__device__ inline uint32_t find_item(const ClipList& l, uint32_t chunk) {
-  uint32_t lo = 0, hi = l.count - 1;  // last item with first <= chunk (no item is empty)
-  while (lo < hi) {
-    const uint32_t mid = (lo + hi + 1) >> 1;
-    if (l.item[mid].first <= chunk) lo = mid;
-    else hi = mid - 1;
+// The last item with first <= chunk (no item is empty).  Every lane compares
+// two of the starts and the wave counts them: two loads in parallel, where a
+// binary search waits for seven.
+struct ClipFinder {
+  uint32_t a, b;
+  __device__ ClipFinder(const ClipList& l) {
+    const uint32_t lane = threadIdx.x & 63u;
+    a = lane < l.count ? l.first[lane] : ~0u;
+    b = lane + 64u < l.count ? l.first[lane + 64u < kClipItems ? lane + 64u : 0u] : ~0u;
   }
-  return lo;
-}
+  __device__ uint32_t operator()(uint32_t chunk) const {
+    return (uint32_t)(__popcll(__ballot(a <= chunk)) + __popcll(__ballot(b <= chunk))) - 1u;
+  }
+};
 
 __device__ inline double wave_sum(double v) {
 #pragma unroll
@@ -101,10 +108,12 @@ __device__ inline double chunk_square_sum(const T* p, int64_t len) {
 __global__ __launch_bounds__(kClipThreads) void k_grad_square_sum(const ClipList l,
                                                                   double* __restrict__ parts) {
   __shared__ double lds4[4];
+  const ClipFinder find(l);
   double acc = 0.0;
   for (uint32_t c = blockIdx.x; c < l.chunks; c += gridDim.x) {
-    const ClipItem& it = l.item[find_item(l, c)];
-    const int64_t at = (int64_t)(c - it.first) * kClipChunk;
+    const uint32_t i = find(c);
+    const ClipItem& it = l.item[i];
+    const int64_t at = (int64_t)(c - l.first[i]) * kClipChunk;
     const int64_t len = it.n - at < kClipChunk ? it.n - at : kClipChunk;
     switch (it.types & 0xFFu) {
       case EMB_F32: acc += chunk_square_sum(static_cast<const float*>(it.in) + at, len); break;
@@ -116,23 +125,18 @@ __global__ __launch_bounds__(kClipThreads) void k_grad_square_sum(const ClipList
   if (threadIdx.x == 0) parts[blockIdx.x] = acc;
 }
 
-__global__ __launch_bounds__(kClipThreads) void k_clip_coef(const double* __restrict__ parts,
-                                                            uint32_t num_parts,
-                                                            const double* __restrict__ extra,
-                                                            int32_t num_extra, float max_norm,
-                                                            float* __restrict__ norm_out) {
-  __shared__ double lds4[4];
+// The norm and the coefficient from the partial sums, the same in every thread
+// of every block that forms them.
+__device__ inline float2 norm_and_coef(const double* __restrict__ parts, uint32_t num_parts,
+                                       const double* __restrict__ extra, int32_t num_extra,
+                                       float max_norm, double* lds4) {
   double acc = 0.0;
   for (uint32_t i = threadIdx.x; i < num_parts; i += kClipThreads) acc += parts[i];
   for (int32_t i = threadIdx.x; i < num_extra; i += kClipThreads) acc += extra[i];
-  acc = block_sum(acc, lds4);
-  if (threadIdx.x == 0) {
-    const double norm = sqrt(acc);
-    double c = (double)max_norm / (norm + 1e-6);
-    c = c < 1.0 ? c : 1.0;
-    norm_out[0] = (float)norm;
-    norm_out[1] = __builtin_isfinite(norm) ? (float)c : 0.0f;
-  }
+  const double norm = sqrt(block_sum(acc, lds4));
+  double c = (double)max_norm / (norm + 1e-6);
+  c = c < 1.0 ? c : 1.0;
+  return make_float2((float)norm, __builtin_isfinite(norm) ? (float)c : 0.0f);
 }
 
 // Elements of one access: 16 bytes of the wider of the two types.
@@ -181,18 +185,33 @@ __device__ inline void scale_item(const ClipItem& it, int64_t at, int64_t len, f
   }
 }
 
-__global__ __launch_bounds__(kClipThreads) void k_clip_scale(const ClipList l,
-                                                             const float* __restrict__ norm) {
-  const float c = norm[1];
-  const uint32_t chunk = l.chunks - 1u - blockIdx.x;
-  const ClipItem& it = l.item[find_item(l, chunk)];
-  if (it.in == it.out && c == 1.0f) return;  // in place and not clipped: already there
-  const int64_t at = (int64_t)(chunk - it.first) * kClipChunk;
-  const int64_t len = it.n - at < kClipChunk ? it.n - at : kClipChunk;
-  switch (it.types & 0xFFu) {
-    case EMB_F32: scale_item<float>(it, at, len, c); break;
-    case EMB_BF16: scale_item<bf16_t>(it, at, len, c); break;
-    default: scale_item<f16_t>(it, at, len, c); break;
+// Every block forms the coefficient itself (at most a few thousand sums, which
+// its L2 holds), so no launch stands between the sum and the scale; the first
+// block of the first launch stores it.  The chunks go from the last one back:
+// what the sum read last is still in the cache.
+__global__ __launch_bounds__(kClipThreads) void k_clip_scale(
+    const ClipList l, const double* __restrict__ parts, uint32_t num_parts,
+    const double* __restrict__ extra, int32_t num_extra, float max_norm,
+    float* __restrict__ norm_out) {
+  __shared__ double lds4[4];
+  const ClipFinder find(l);
+  const float2 nc = norm_and_coef(parts, num_parts, extra, num_extra, max_norm, lds4);
+  const float c = nc.y;
+  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) {
+    norm_out[0] = nc.x;
+    norm_out[1] = c;
+  }
+  for (uint32_t k = blockIdx.x; k < l.chunks; k += gridDim.x) {
+    const uint32_t chunk = l.chunks - 1u - k, i = find(chunk);
+    const ClipItem& it = l.item[i];
+    if (it.in == it.out && c == 1.0f) continue;  // in place and not clipped: already there
+    const int64_t at = (int64_t)(chunk - l.first[i]) * kClipChunk;
+    const int64_t len = it.n - at < kClipChunk ? it.n - at : kClipChunk;
+    switch (it.types & 0xFFu) {
+      case EMB_F32: scale_item<float>(it, at, len, c); break;
+      case EMB_BF16: scale_item<bf16_t>(it, at, len, c); break;
+      default: scale_item<f16_t>(it, at, len, c); break;
+    }
   }
 }
 
@@ -205,11 +224,11 @@ bool next_list(const emb_tensor_t* grads, const emb_tensor_t* out, int32_t n, in
     if (g.numel == 0) continue;
     const int64_t chunks = (g.numel + kClipChunk - 1) / kClipChunk;
     if ((int64_t)l->chunks + chunks > 0x7FFFFFFF) break;  // the next launch takes it
-    ClipItem& it = l->item[l->count++];
+    ClipItem& it = l->item[l->count];
+    l->first[l->count++] = l->chunks;
     it.in = g.data;
     it.out = out ? out[*at].data : nullptr;
     it.n = g.numel;
-    it.first = l->chunks;
     it.types = (uint32_t)g.dtype | (uint32_t)(out ? out[*at].dtype : 0) << 8;
     l->chunks += (uint32_t)chunks;
   }
@@ -243,13 +262,17 @@ hipError_t launch_clip_grad_norm(const emb_tensor_t* grads, const emb_tensor_t* 
                        parts + num_parts);
     num_parts += grid;
   }
-  hipLaunchKernelGGL(k_clip_coef, dim3(1), dim3(kClipThreads), 0, s, parts, num_parts, extra,
-                     num_extra, max_norm, norm_out);
-  if (out) {
-    at = 0;
-    while (next_list(grads, out, n, &at, &l))
-      hipLaunchKernelGGL(k_clip_scale, dim3(l.chunks), dim3(kClipThreads), 0, s, l, norm_out);
-  }
+  // the coefficient is wanted without an output too: then of an empty list
+  at = out ? 0 : n;
+  bool more = next_list(grads, out, n, &at, &l);
+  float* store = norm_out;
+  do {
+    const unsigned grid = l.chunks < (unsigned)kScaleBlocks ? l.chunks : (unsigned)kScaleBlocks;
+    hipLaunchKernelGGL(k_clip_scale, dim3(grid ? grid : 1u), dim3(kClipThreads), 0, s, l, parts,
+                       num_parts, extra, num_extra, max_norm, store);
+    store = nullptr;
+    more = more && next_list(grads, out, n, &at, &l);
+  } while (more);
   return hipGetLastError();
 }
 
