@@ -72,11 +72,19 @@ bool make_plan(const Handle& h, int64_t B, int64_t nnz, Plan* p) {
     p->shift[i] = sh;
     sh += p->dbits[i];
   }
-  p->ntiles = (nnz + kSortTile - 1) / kSortTile;
+  p->sort_items = nnz > kSortTile && nnz <= kSmallSortMax ? kSmallSortItems : kSortItems;
+  const int64_t tile = (int64_t)kSortThreads * p->sort_items;
+  p->ntiles = (nnz + tile - 1) / tile;
   p->chunk = chunk_len(h.D);
   p->nchunks = (nnz + p->chunk - 1) / p->chunk;
   const size_t n4 = sizeof(uint32_t) * (size_t)(nnz > 0 ? nnz : 1);
-  const size_t nt = (size_t)(p->ntiles > 0 ? p->ntiles : 1);
+  // a longer batch's workspace also serves every shorter one, whose tiles may
+  // be smaller and more
+  const int64_t small_tile = (int64_t)kSortThreads * kSmallSortItems;
+  const int64_t small = nnz < kSmallSortMax ? nnz : kSmallSortMax;
+  int64_t most_tiles = (small + small_tile - 1) / small_tile;
+  if (most_tiles < p->ntiles) most_tiles = p->ntiles;
+  const size_t nt = (size_t)(most_tiles > 0 ? most_tiles : 1);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     size_t at = o;

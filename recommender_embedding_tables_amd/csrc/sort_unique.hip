@@ -13,7 +13,7 @@
 //                   s*T + t and, for mean pooling, 1/L of its bag; flags the
 //                   batch as not one-hot when a bag's length is not 1.  The
 //                   sort's value of occurrence j is j itself (not stored).
-//   k_sort_hist     per 4096-key tile, digit counts -> tile_hist[digit][tile].
+//   k_sort_hist     per 4096-key tile (1024 in smaller batches), digit counts -> tile_hist[digit][tile].
 //   k_sort_scan     one block per digit: exclusive scan over tiles, digit totals.
 //   k_sort_scatter  per tile: stable rank of every key (per-wave ballot match
 //                   of the digit, waves own contiguous quarters of the tile),
@@ -189,6 +189,7 @@ __device__ inline uint64_t match_digit(uint32_t d, bool valid, int nbits) {
   return m;
 }
 
+template <int ITEMS>
 __global__ __launch_bounds__(256) void k_sort_hist(const uint32_t* __restrict__ keys, uint32_t n,
                                                    int shift, int nbits,
                                                    uint32_t* __restrict__ tile_hist,
@@ -201,16 +202,16 @@ __global__ __launch_bounds__(256) void k_sort_hist(const uint32_t* __restrict__ 
   // XCD-contiguous tiles: the per-digit counts of neighbouring tiles share
   // cache lines of tile_hist
   const uint32_t tile = xcd_block();
-  const uint32_t base = tile * (uint32_t)kSortTile + (uint32_t)w * (kSortItems * 64);
-  uint32_t kv[kSortItems];
+  const uint32_t base = tile * (256u * ITEMS) + (uint32_t)w * (ITEMS * 64);
+  uint32_t kv[ITEMS];
 #pragma unroll
-  for (int r = 0; r < kSortItems; ++r) {
+  for (int r = 0; r < ITEMS; ++r) {
     const uint32_t idx = base + r * 64 + lane;
     kv[r] = idx < n ? keys[idx] : 0u;
   }
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < kSortItems; ++r) {
+  for (int r = 0; r < ITEMS; ++r) {
     const uint32_t idx = base + r * 64 + lane;
     const bool valid = idx < n;
     const uint32_t d = (kv[r] >> shift) & mask;
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(256) void k_sort_scan(uint32_t* __restrict__ tile_h
 // coalesced loads; a stale occurrence index gets the invalid grad row
 // 0xFFFFFFFF.  When every bag holds one id (a flag of k_keys) the grad row
 // follows from the occurrence index and the consumers compute it from perm.
-template <bool FIRST>
+template <bool FIRST, int ITEMS>
 __global__ __launch_bounds__(256) void k_sort_scatter(
     const uint32_t* __restrict__ keys_in, const uint32_t* __restrict__ vals_in,
     uint32_t* __restrict__ keys_out, uint32_t* __restrict__ vals_out, uint32_t n, int shift,
@@ -267,8 +268,8 @@ __global__ __launch_bounds__(256) void k_sort_scatter(
   __shared__ uint32_t whist[4][kMaxRadix];
   __shared__ uint32_t dstart[kMaxRadix];
   __shared__ uint32_t gbase[kMaxRadix];
-  __shared__ uint32_t skeys[kSortTile];
-  __shared__ uint32_t svals[kSortTile];
+  __shared__ uint32_t skeys[256 * ITEMS];
+  __shared__ uint32_t svals[256 * ITEMS];
   __shared__ uint32_t lds4[4];
   const int radix = 1 << nbits;
   const uint32_t mask = (uint32_t)radix - 1u;
@@ -277,10 +278,10 @@ __global__ __launch_bounds__(256) void k_sort_scatter(
   // lines of the output, so their partial-line stores meet in one L2
   const uint32_t tile = xcd_block();
   for (int i = threadIdx.x; i < 4 * kMaxRadix; i += 256) (&whist[0][0])[i] = 0u;
-  const uint32_t base = tile * (uint32_t)kSortTile + (uint32_t)w * (kSortItems * 64);
-  uint32_t kv[kSortItems], vv[kSortItems], lr[kSortItems];
+  const uint32_t base = tile * (256u * ITEMS) + (uint32_t)w * (ITEMS * 64);
+  uint32_t kv[ITEMS], vv[ITEMS], lr[ITEMS];
 #pragma unroll
-  for (int r = 0; r < kSortItems; ++r) {
+  for (int r = 0; r < ITEMS; ++r) {
     const uint32_t idx = base + r * 64 + lane;
     kv[r] = 0u;
     vv[r] = idx;
@@ -292,7 +293,7 @@ __global__ __launch_bounds__(256) void k_sort_scatter(
   __syncthreads();
   // Stable rank inside the wave's quarter: rounds go in position order.
 #pragma unroll
-  for (int r = 0; r < kSortItems; ++r) {
+  for (int r = 0; r < ITEMS; ++r) {
     const uint32_t idx = base + r * 64 + lane;
     const bool valid = idx < n;
     const uint32_t d = (kv[r] >> shift) & mask;
@@ -336,7 +337,7 @@ __global__ __launch_bounds__(256) void k_sort_scatter(
   }
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < kSortItems; ++r) {
+  for (int r = 0; r < ITEMS; ++r) {
     const uint32_t idx = base + r * 64 + lane;
     if (idx < n) {
       const uint32_t d = (kv[r] >> shift) & mask;
@@ -346,8 +347,8 @@ __global__ __launch_bounds__(256) void k_sort_scatter(
     }
   }
   __syncthreads();
-  const uint32_t tbase = tile * (uint32_t)kSortTile;
-  const uint32_t tn = (n - tbase) < (uint32_t)kSortTile ? (n - tbase) : (uint32_t)kSortTile;
+  const uint32_t tbase = tile * (256u * ITEMS);
+  const uint32_t tn = (n - tbase) < 256u * ITEMS ? (n - tbase) : 256u * ITEMS;
   const bool one_hot = gr_out && !batch_not_one_hot(misc);
   for (uint32_t i = threadIdx.x; i < tn; i += 256) {
     const uint32_t k = skeys[i];
@@ -583,6 +584,7 @@ const Handle& h, const Plan& p, const int64_t* offsets,
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const uint32_t ntiles = (uint32_t)p.ntiles;
+  const bool small = p.sort_items == kSmallSortItems;
   uint32_t* kin = kA;
   uint32_t* vin = vA;
   uint32_t* kout = kB;
@@ -592,24 +594,28 @@ const Handle& h, const Plan& p, const int64_t* offsets,
     for (int pass = 0; pass < p.passes; ++pass) {
       const int radix = 1 << p.dbits[pass];
       if (ntiles > 1) {  // a single tile ranks itself inside the scatter
-        hipLaunchKernelGGL(k_sort_hist, dim3(ntiles), dim3(256), 0, s, kin, n, p.shift[pass],
-                           p.dbits[pass], tile_hist, ntiles);
+        if (small)
+          hipLaunchKernelGGL((k_sort_hist<kSmallSortItems>), dim3(ntiles), dim3(256), 0, s, kin, n,
+                             p.shift[pass], p.dbits[pass], tile_hist, ntiles);
+        else
+          hipLaunchKernelGGL((k_sort_hist<kSortItems>), dim3(ntiles), dim3(256), 0, s, kin, n,
+                             p.shift[pass], p.dbits[pass], tile_hist, ntiles);
         hipLaunchKernelGGL(k_sort_scan, dim3(radix), dim3(256), 0, s, tile_hist, ntiles,
                            digit_tot);
       }
       const bool last = pass + 1 == p.passes;
       uint32_t* gro = last ? reinterpret_cast<uint32_t*>(ws + p.sgr) : nullptr;
       float* sco = (last && mean) ? reinterpret_cast<float*>(ws + p.sscale) : nullptr;
-      if (pass == 0)
-        hipLaunchKernelGGL(k_sort_scatter<true>, dim3(ntiles), dim3(256), 0, s, kin, vin, kout,
-                           vout, n, p.shift[pass], p.dbits[pass], tile_hist, digit_tot, ntiles, gr,
-                           gro, sco, misc, (uint32_t)p.B, (uint32_t)h.T, in_place_blk,
-                           (uint32_t)bpb, kgrid);
-      else
-        hipLaunchKernelGGL(k_sort_scatter<false>, dim3(ntiles), dim3(256), 0, s, kin, vin, kout,
-                           vout, n, p.shift[pass], p.dbits[pass], tile_hist, digit_tot, ntiles, gr,
-                           gro, sco, misc, (uint32_t)p.B, (uint32_t)h.T, in_place_blk,
-                           (uint32_t)bpb, kgrid);
+#define EMBTAB_SCATTER(FIRST_, ITEMS_)                                                            \
+  hipLaunchKernelGGL((k_sort_scatter<FIRST_, ITEMS_>), dim3(ntiles), dim3(256), 0, s, kin, vin,   \
+                     kout, vout, n, p.shift[pass], p.dbits[pass], tile_hist, digit_tot, ntiles,   \
+                     gr, gro, sco, misc, (uint32_t)p.B, (uint32_t)h.T, in_place_blk,              \
+                     (uint32_t)bpb, kgrid)
+      if (pass == 0 && small) EMBTAB_SCATTER(true, kSmallSortItems);
+      else if (pass == 0) EMBTAB_SCATTER(true, kSortItems);
+      else if (small) EMBTAB_SCATTER(false, kSmallSortItems);
+      else EMBTAB_SCATTER(false, kSortItems);
+#undef EMBTAB_SCATTER
       e = hipGetLastError();
       if (e != hipSuccess) return e;
       uint32_t* tk = kin;
