@@ -38,6 +38,12 @@ constexpr int kTileThreads = 256;
 constexpr int kTileRounds = 4;
 constexpr int kTile = kTileThreads * kTileRounds;
 constexpr int kMaxExperts = 1024;
+// Up to this many tiles every block of the scatter adds the tiles' counts
+// itself (counts [tile][expert], one row per tile) and the scan's launch is
+// saved: sort, dispatch and combine of 4096 tokens with two choices take 19 us
+// against 21.5, of 16384 tokens 22.5 against 23.8; with more tiles the adding
+// takes as long as the scan (counts [expert][tile]).
+constexpr uint32_t kDirectTiles = 32;
 
 __device__ inline uint32_t expert_block_scan(uint32_t v, uint32_t* total, uint32_t* lds4) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -71,7 +77,8 @@ __global__ __launch_bounds__(kTileThreads) void k_expert_hist(const int64_t* __r
   }
   __syncthreads();
   for (uint32_t e = threadIdx.x; e < experts; e += kTileThreads)
-    tile_hist[(size_t)e * ntiles + blockIdx.x] = cnt[e];
+    tile_hist[ntiles <= kDirectTiles ? (size_t)blockIdx.x * experts + e
+                                     : (size_t)e * ntiles + blockIdx.x] = cnt[e];
 }
 
 // One block per expert: exclusive scan of its counts over the tiles.
@@ -142,12 +149,25 @@ __global__ __launch_bounds__(kTileThreads) void k_expert_scatter(
     uint32_t keep = 0u;
     if (e < experts) {
       const uint32_t c0 = wcnt[0][e], c1 = wcnt[1][e], c2 = wcnt[2][e], c3 = wcnt[3][e];
-      const uint32_t t0 = solo ? 0u : tile_off[(size_t)e * ntiles + blockIdx.x];
+      uint32_t t0 = 0u, all = 0u;  // choices of the earlier tiles and of all
+      if (solo) {
+        all = c0 + c1 + c2 + c3;
+      } else if (ntiles <= kDirectTiles) {
+#pragma unroll 8
+        for (uint32_t t = 0; t < ntiles; ++t) {
+          const uint32_t v = tile_off[(size_t)t * experts + e];
+          t0 += t < blockIdx.x ? v : 0u;
+          all += v;
+        }
+      } else {
+        t0 = tile_off[(size_t)e * ntiles + blockIdx.x];
+        all = totals[e];
+      }
       wcnt[0][e] = t0;
       wcnt[1][e] = t0 + c0;
       wcnt[2][e] = t0 + c0 + c1;
       wcnt[3][e] = t0 + c0 + c1 + c2;
-      keep = solo ? c0 + c1 + c2 + c3 : totals[e];
+      keep = all;
       if (capacity && (int64_t)keep > capacity) keep = (uint32_t)capacity;
       kept[e] = keep;
     }
@@ -573,8 +593,9 @@ hipError_t launch_expert_sort(const int64_t* ids, int64_t tokens, int32_t topk, 
   if (tiles > 1u) {
     hipLaunchKernelGGL(k_expert_hist, dim3(tiles), dim3(kTileThreads), 0, s, ids, n,
                        (uint32_t)experts, tiles, hist);
-    hipLaunchKernelGGL(k_expert_scan, dim3((unsigned)experts), dim3(kTileThreads), 0, s, hist,
-                       tiles, totals);
+    if (tiles > kDirectTiles)
+      hipLaunchKernelGGL(k_expert_scan, dim3((unsigned)experts), dim3(kTileThreads), 0, s, hist,
+                         tiles, totals);
   }
   hipLaunchKernelGGL(k_expert_scatter, dim3(tiles), dim3(kTileThreads), 0, s, ids, n,
                      (uint32_t)experts, nbits, capacity, rows, tiles, hist, totals, offsets, src,
