@@ -78,13 +78,8 @@ bool make_plan(const Handle& h, int64_t B, int64_t nnz, Plan* p) {
   p->chunk = chunk_len(h.D);
   p->nchunks = (nnz + p->chunk - 1) / p->chunk;
   const size_t n4 = sizeof(uint32_t) * (size_t)(nnz > 0 ? nnz : 1);
-  // a longer batch's workspace also serves every shorter one, whose tiles may
-  // be smaller and more
-  const int64_t small_tile = (int64_t)kSortThreads * kSmallSortItems;
-  const int64_t small = nnz < kSmallSortMax ? nnz : kSmallSortMax;
-  int64_t most_tiles = (small + small_tile - 1) / small_tile;
-  if (most_tiles < p->ntiles) most_tiles = p->ntiles;
-  const size_t nt = (size_t)(most_tiles > 0 ? most_tiles : 1);
+  const int64_t full_tiles = (nnz + kSortTile - 1) / kSortTile;
+  const size_t nt = (size_t)(full_tiles > 0 ? full_tiles : 1);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     size_t at = o;
@@ -103,6 +98,12 @@ bool make_plan(const Handle& h, int64_t B, int64_t nnz, Plan* p) {
   p->tile_hist = take(sizeof(uint32_t) * kMaxRadix * nt);
   p->digit_tot = take(sizeof(uint32_t) * kMaxRadix);
   p->unique = take(n4);
+  // The counts of small tiles, four times as many, lie in the space of the
+  // unique rows, which are written after the sort: 2048 bytes per 1024 keys
+  // of 4 bytes each (and there are more than 4096).
+  static_assert(sizeof(uint32_t) * kMaxRadix * 2 <= sizeof(uint32_t) * kSortThreads * kSmallSortItems,
+                "a tile's counts take half of its keys' space");
+  if (p->sort_items == kSmallSortItems) p->tile_hist = p->unique;
   p->seg_off = take(n4 + sizeof(uint32_t));
   p->counts = take(n4);
   p->inverse = take(n4);

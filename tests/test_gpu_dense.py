@@ -725,3 +725,77 @@ def test_another_stream_and_a_graph_give_the_eager_bits():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(results(s), want)), f"replay {r}"
         del scratch
+
+
+# ---------------------------------------------------------------- values at the edges
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("dim", [24, 479, 1664])
+def test_gates_that_are_infinite_or_nan(kind, dim):
+    """A sigmoid gate of -inf shuts the branch, +inf opens it; a NaN stays in its element's row."""
+    t, n = TYPES[kind], 8
+    x, block, gt, w_post, scale, w_pre, dy, dh = norm_inputs(3, n, dim, t, "element", True)
+    gt = gt.clone()
+    gt[0], gt[1], gt[2], gt[3] = -float("inf"), float("inf"), -200.0, 200.0
+    gt[4, 5] = float("nan")
+    y, h = torch.empty_like(x), torch.empty_like(x)
+    code = eb.EMB_GATE_ELEMENT | eb.EMB_GATE_SIGMOID
+    eb.check(eb.emb_gated_norm_forward(x, block, gt, w_post, scale, w_pre, n, dim,
+                                       eb.dtype_code(t), code, 1e-6, y, h), "forward")
+    open_, h1 = torch.empty_like(x), torch.empty_like(x)
+    eb.check(eb.emb_gated_norm_forward(x, block, None, w_post, scale, w_pre, n, dim,
+                                       eb.dtype_code(t), eb.EMB_GATE_NONE, 1e-6, open_, h1), "open")
+    torch.cuda.synchronize()
+    assert torch.equal(y[0], x[0]) and torch.equal(y[2], x[2])
+    assert torch.equal(y[1], open_[1]) and torch.equal(y[3], open_[3])
+    assert torch.equal(h[1], h1[1])
+    nan = torch.isnan(y)
+    assert bool(nan[4, 5]) and int(nan.sum()) == 1
+    assert bool(torch.isnan(h[4]).all()) and int(torch.isnan(h).sum()) == dim
+    # gradients: a saturated gate passes none back, an open one the whole of it
+    dx, db, dg = (torch.empty_like(x) for _ in range(3))
+    sums = torch.empty(3, dim, device=DEV)
+    need = eb.emb_gated_norm_workspace_bytes(n, dim)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV).fill_(255)
+    gt[4, 5] = 0.0
+    eb.check(eb.emb_gated_norm_backward(x, block, gt, w_post, scale, w_pre, dy, dh, n, dim,
+                                        eb.dtype_code(t), code, 1e-6, dx, db, dg, *sums, ws, need),
+             "backward")
+    torch.cuda.synchronize()
+    assert (dg[:4] == 0).all() and (db[0] == 0).all() and (db[2] == 0).all()
+    assert all(torch.isfinite(v).all() for v in (dx, db, dg, sums))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [1e-15, 1e-19, 1e15])
+def test_norm_of_rows_far_from_one(kind, scale):
+    """Mean squares from 1e-38, where fp32 has few bits left, up to 1e30, without an eps."""
+    t, n, dim = TYPES[kind], 6, 512
+    x = rand(gen(5), n, dim, scale=scale).to(t)
+    zero = torch.zeros_like(x)
+    one = torch.ones(dim, device=DEV)
+    y, h = torch.empty_like(x), torch.empty_like(x)
+    eb.check(eb.emb_gated_norm_forward(x, zero, None, None, one, one, n, dim, eb.dtype_code(t),
+                                       eb.EMB_GATE_NONE, 0.0, y, h), "forward")
+    torch.cuda.synchronize()
+    assert torch.equal(x, y)
+    ref = x.double() * rms_inv(x.double(), 0.0)
+    # each square of 1e-38 keeps |x|^2 / 2^-150 steps: half of one, over the mean
+    low = 2.0 ** -150 / (x.double() ** 2).mean(1, keepdim=True) if scale < 1e-17 else 0.0
+    within(h, ref, ref.abs() * ((sum_steps(dim, t) / 2 + 4) * U + low), "h")
+
+
+def test_clip_of_more_chunks_than_blocks():
+    """Lists of more than 2048 chunks of 8192 elements, which the blocks take in turn."""
+    g = gen(21)
+    grads = [rand(g, 18_000_007, scale=0.01), rand(g, 3_000_001, scale=0.5).to(torch.bfloat16)]
+    ref, coef = plain_clip(grads, 1.0)
+    norm, outs = run_clip(grads, [torch.float32, torch.float32], 1.0)
+    assert abs(float(norm[0]) - ref) <= 1.01 * U * ref
+    for x, o in zip(grads, outs):
+        r = x.double() * coef
+        within(o, r, 2.02 * U * r.abs() + TINY[torch.float32], "scaled")
+    want = [o.clone() for o in outs]
+    same = [x.clone() for x in grads]
+    run_clip(same[:1], [torch.float32], 1e9, in_place=True)
+    assert torch.equal(same[0], grads[0]) and all(torch.equal(a, b) for a, b in zip(want, outs))
