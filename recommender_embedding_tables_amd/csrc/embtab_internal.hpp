@@ -32,10 +32,15 @@ constexpr int kSortTile = kSortThreads * kSortItems;
 // Sort tiles of batches up to kSmallSortMax keys: a quarter of the size, since
 // tiles of 4096 keys leave most CUs idle and each waits for 16 rounds of
 // ranking (three passes over 320 thousand keys: 89 us with 16 keys per thread,
-// 57 with 4; 1.7 million: 113 and 98; 2.6 million: 5 us apart).  A batch of one
-// large tile keeps it: it needs no histogram and no scan.
+// 57 with 4; the 131-thousand-key step of two tables of 5e7 rows: 0.258 and
+// 0.222 ms, and with its prepares beside other steps 0.205 and 0.180).  Longer
+// batches fill the chip with large tiles too; small ones still sort 1.7 million
+// keys 15 us sooner alone, but beside another stream's kernels they slow those
+// more than that (that step 0.551 -> 0.564 ms, 2.6 million keys 0.344 ->
+// 0.374).  A batch of one large tile keeps it: it needs no histogram and no
+// scan.
 constexpr int kSmallSortItems = 4;
-constexpr int64_t kSmallSortMax = 1 << 22;
+constexpr int64_t kSmallSortMax = 1 << 19;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxRadix = 1 << kMaxDigitBits;
 

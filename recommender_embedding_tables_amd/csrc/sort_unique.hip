@@ -13,7 +13,8 @@
 //                   s*T + t and, for mean pooling, 1/L of its bag; flags the
 //                   batch as not one-hot when a bag's length is not 1.  The
 //                   sort's value of occurrence j is j itself (not stored).
-//   k_sort_hist     per 4096-key tile (1024 in smaller batches), digit counts -> tile_hist[digit][tile].
+//   k_sort_hist     per tile of 4096 keys (1024 in batches of up to 2^19),
+//                   digit counts -> tile_hist[digit][tile].
 //   k_sort_scan     one block per digit: exclusive scan over tiles, digit totals.
 //   k_sort_scatter  per tile: stable rank of every key (per-wave ballot match
 //                   of the digit, waves own contiguous quarters of the tile),

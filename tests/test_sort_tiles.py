@@ -1,4 +1,4 @@
-"""Sort tiles of both sizes (1024 keys up to 2^22 keys, 4096 beyond and for one
+"""Sort tiles of both sizes (1024 keys up to 2^19 keys, 4096 beyond and for one
 tile): the sorted positions and their runs against numpy's stable sort at the
 edges, and a workspace that a shorter batch never outgrows."""
 import ctypes as C
@@ -10,7 +10,7 @@ import torch
 eb = pytest.importorskip("recommender_embedding_tables_amd.embtab",
                          reason="libembtab.so not built")
 
-EDGE = 1 << 22
+EDGE = 1 << 19
 
 
 def test_a_longer_batch_never_needs_less_workspace():
@@ -29,7 +29,7 @@ def test_a_longer_batch_never_needs_less_workspace():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("n", [4096, 4097, 5121, 300_001, EDGE, EDGE + 1])
+@pytest.mark.parametrize("n", [4096, 4097, 5121, 300_001, EDGE, EDGE + 1, (1 << 22) + 1])
 @pytest.mark.parametrize("rows", [[700, 90], [200_000, 3, 1_500_000]])
 def test_sorted_positions(n, rows):
     dev = torch.device("cuda")
