@@ -18,20 +18,21 @@
 //   dw_post = sum_rows du * ohat;  dscale = sum_rows t * a * u;
 //   dw_pre = sum_rows dh * yhat
 //
-// Bound by memory: each stream is read or written once (a large device copy
-// reaches 5.2 TB/s here).  A row's vectors live in the registers of the threads
+// Bound by memory: each stream is read or written once (by the counters too; a
+// one-shot device copy reaches 6.5 TB/s here).  A row's vectors live in the registers of the threads
 // that share it (lanes of one wave for short rows, the whole block for long
 // ones), so the statistics and the results come from one read, and the loads
 // of a thread's next row are issued with the stores of this one.  Issuing them
 // a row ahead, into a second set of registers, left fewer waves and gained
-// nothing (32768 x 3328 bf16: 214 us against 210).  The blocks walk over rows
+// nothing (same rows: 214 us against 210 on the same buffers).  The blocks walk over rows
 // and keep the weights of their columns, and in the backward pass the columns'
 // sums.  The sums of a block go to the workspace and a second kernel adds them
 // in block order: no atomics, the result does not depend on timing.
 //
 // Element-wise sigmoid gate, norm before the gate:
-//   forward   32768 x 3328 bf16   210 us, 5.2 TB/s
-//   backward  16384 x 3328 bf16   187 us, 4.7 TB/s (its column sums 11 us of it)
+//   forward   32768 x 3328 bf16   185 us, 5.9 TB/s (210 us where all five
+//             streams begin at the same offset of a large power of two)
+//   backward  16384 x 3328 bf16   173 us, 5.0 TB/s, and 6 us for the column sums
 // What moved them there: sums by lane permutations in place of LDS shuffles,
 // the hardware's exponential and reciprocal for 16-bit gates, weights in LDS.
 #include "dense.hpp"

