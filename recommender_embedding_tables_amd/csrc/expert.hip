@@ -214,6 +214,17 @@ __device__ inline uint32_t vec_column(uint32_t v, uint32_t dim) {
 }
 
 constexpr int kRowThreads = 256;
+
+// A launch holds fewer than 2^32 threads along x: more blocks of the row
+// kernels than that go along y too.  Block indexes past the last one find no
+// token and no row.
+constexpr int64_t kGridX = 1 << 23;
+__device__ inline uint32_t block_index() { return blockIdx.y * gridDim.x + blockIdx.x; }
+dim3 row_grid(int64_t blocks) {
+  return blocks <= kGridX ? dim3((unsigned)blocks)
+                          : dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
+}
+
 constexpr int kRowVecs = 4;          // vectors in flight per thread
 constexpr uint32_t kWideVecs = 64;   // vectors of a row that takes a wave of its own
 constexpr uint32_t kZeroRows = 64;   // rows checked by one zero-fill block
@@ -243,11 +254,12 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_dispatch(
     const T* __restrict__ x, const int32_t* __restrict__ pos, const int32_t* __restrict__ src,
     int64_t tokens, uint32_t topk, int64_t rows, uint32_t dim, uint32_t nvec, uint32_t tpb,
     uint32_t token_blocks, T* __restrict__ xs) {
-  if (blockIdx.x >= token_blocks) {
-    zero_empty_rows(src, (int64_t)(blockIdx.x - token_blocks) * kZeroRows, rows, dim, xs);
+  const uint32_t block = block_index();
+  if (block >= token_blocks) {
+    zero_empty_rows(src, (int64_t)(block - token_blocks) * kZeroRows, rows, dim, xs);
     return;
   }
-  const int64_t t0 = (int64_t)blockIdx.x * tpb;
+  const int64_t t0 = (int64_t)block_index() * tpb;
   const uint32_t nt = tokens - t0 < (int64_t)tpb ? (uint32_t)(tokens - t0) : tpb;
   const uint32_t all = nt * nvec;
   for (uint32_t i0 = threadIdx.x; i0 < all; i0 += kRowThreads * kRowVecs) {
@@ -278,12 +290,13 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_dispatch_wide(
     const T* __restrict__ x, const int32_t* __restrict__ pos, const int32_t* __restrict__ src,
     int64_t tokens, uint32_t topk, int64_t rows, uint32_t dim, uint32_t nvec,
     uint32_t token_blocks, T* __restrict__ xs) {
-  if (blockIdx.x >= token_blocks) {
-    zero_empty_rows(src, (int64_t)(blockIdx.x - token_blocks) * kZeroRows, rows, dim, xs);
+  const uint32_t block = block_index();
+  if (block >= token_blocks) {
+    zero_empty_rows(src, (int64_t)(block - token_blocks) * kZeroRows, rows, dim, xs);
     return;
   }
   const uint32_t lane = threadIdx.x & 63u;
-  const int64_t tok = (int64_t)blockIdx.x * (kRowThreads / 64) +
+  const int64_t tok = (int64_t)block_index() * (kRowThreads / 64) +
                       __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (tok >= tokens) return;
   const int32_t* p = pos + (size_t)tok * topk;
@@ -313,7 +326,8 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_combine(
     const T* __restrict__ ys, const int32_t* __restrict__ pos, const float* __restrict__ weights,
     int64_t tokens, uint32_t topk, uint32_t rows, uint32_t dim, uint32_t nvec, uint32_t tpb,
     T* __restrict__ y) {
-  const int64_t t0 = (int64_t)blockIdx.x * tpb;
+  const int64_t t0 = (int64_t)block_index() * tpb;
+  if (t0 >= tokens) return;
   const uint32_t nt = tokens - t0 < (int64_t)tpb ? (uint32_t)(tokens - t0) : tpb;
   const uint32_t all = nt * nvec;
   for (uint32_t i = threadIdx.x; i < all; i += kRowThreads) {
@@ -359,7 +373,7 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_combine_wide(
     T* __restrict__ y) {
   constexpr int U = K <= 4 ? 4 : 2;
   const uint32_t lane = threadIdx.x & 63u;
-  const int64_t tok = (int64_t)blockIdx.x * (kRowThreads / 64) +
+  const int64_t tok = (int64_t)block_index() * (kRowThreads / 64) +
                       __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (tok >= tokens) return;
   T* row = y + (size_t)tok * dim;
@@ -419,12 +433,13 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_combine_backward(
     const int32_t* __restrict__ src, const float* __restrict__ weights, int64_t tokens,
     uint32_t topk, int64_t rows, uint32_t dim, uint32_t nvec, uint32_t token_blocks,
     T* __restrict__ dys, float* __restrict__ dweights) {
-  if (blockIdx.x >= token_blocks) {
-    zero_empty_rows(src, (int64_t)(blockIdx.x - token_blocks) * kZeroRows, rows, dim, dys);
+  const uint32_t block = block_index();
+  if (block >= token_blocks) {
+    zero_empty_rows(src, (int64_t)(block - token_blocks) * kZeroRows, rows, dim, dys);
     return;
   }
   const uint32_t lane = threadIdx.x & 63u;
-  const int64_t tok = (int64_t)blockIdx.x * (kRowThreads / 64) +
+  const int64_t tok = (int64_t)block_index() * (kRowThreads / 64) +
                       __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (tok >= tokens) return;
   const T* row = dy + (size_t)tok * dim;
@@ -489,11 +504,11 @@ hipError_t dispatch_t(const void* x, const int32_t* pos, const int32_t* src, int
   const int64_t tb = (tokens + per - 1) / per, zb = (rows + kZeroRows - 1) / kZeroRows;
   if (tb + zb == 0) return hipSuccess;
   if (wide)
-    hipLaunchKernelGGL((k_expert_dispatch_wide<T>), dim3((unsigned)(tb + zb)), dim3(kRowThreads),
+    hipLaunchKernelGGL((k_expert_dispatch_wide<T>), row_grid(tb + zb), dim3(kRowThreads),
                        0, s, static_cast<const T*>(x), pos, src, tokens, (uint32_t)topk, rows,
                        (uint32_t)dim, nvec, (uint32_t)tb, static_cast<T*>(xs));
   else
-    hipLaunchKernelGGL((k_expert_dispatch<T>), dim3((unsigned)(tb + zb)), dim3(kRowThreads), 0, s,
+    hipLaunchKernelGGL((k_expert_dispatch<T>), row_grid(tb + zb), dim3(kRowThreads), 0, s,
                        static_cast<const T*>(x), pos, src, tokens, (uint32_t)topk, rows,
                        (uint32_t)dim, nvec, tpb, (uint32_t)tb, static_cast<T*>(xs));
   return hipGetLastError();
@@ -504,25 +519,25 @@ hipError_t combine_k(const void* ys, const int32_t* pos, const float* weights, i
                      int32_t topk, int64_t rows, int32_t dim, void* y, hipStream_t s) {
   const uint32_t nvec = vectors((uint32_t)dim, kVec<T>);
   const uint32_t tpb = tokens_per_block(nvec);
-  const unsigned grid = (unsigned)((tokens + tpb - 1) / tpb);
+  const dim3 grid = row_grid((tokens + tpb - 1) / tpb);
   if (nvec >= kWideVecs) {
-    const unsigned wgrid = (unsigned)((tokens + kRowThreads / 64 - 1) / (kRowThreads / 64));
+    const dim3 wgrid = row_grid((tokens + kRowThreads / 64 - 1) / (kRowThreads / 64));
     if (weights)
-      hipLaunchKernelGGL((k_expert_combine_wide<T, K, true>), dim3(wgrid), dim3(kRowThreads), 0,
+      hipLaunchKernelGGL((k_expert_combine_wide<T, K, true>), wgrid, dim3(kRowThreads), 0,
                          s, static_cast<const T*>(ys), pos, weights, tokens, (uint32_t)topk,
                          (uint32_t)rows, (uint32_t)dim, nvec, static_cast<T*>(y));
     else
-      hipLaunchKernelGGL((k_expert_combine_wide<T, K, false>), dim3(wgrid), dim3(kRowThreads),
+      hipLaunchKernelGGL((k_expert_combine_wide<T, K, false>), wgrid, dim3(kRowThreads),
                          0, s, static_cast<const T*>(ys), pos, weights, tokens, (uint32_t)topk,
                          (uint32_t)rows, (uint32_t)dim, nvec, static_cast<T*>(y));
     return hipGetLastError();
   }
   if (weights)
-    hipLaunchKernelGGL((k_expert_combine<T, K, true>), dim3(grid), dim3(kRowThreads), 0, s,
+    hipLaunchKernelGGL((k_expert_combine<T, K, true>), grid, dim3(kRowThreads), 0, s,
                        static_cast<const T*>(ys), pos, weights, tokens, (uint32_t)topk,
                        (uint32_t)rows, (uint32_t)dim, nvec, tpb, static_cast<T*>(y));
   else
-    hipLaunchKernelGGL((k_expert_combine<T, K, false>), dim3(grid), dim3(kRowThreads), 0, s,
+    hipLaunchKernelGGL((k_expert_combine<T, K, false>), grid, dim3(kRowThreads), 0, s,
                        static_cast<const T*>(ys), pos, weights, tokens, (uint32_t)topk,
                        (uint32_t)rows, (uint32_t)dim, nvec, tpb, static_cast<T*>(y));
   return hipGetLastError();
@@ -546,7 +561,7 @@ hipError_t combine_backward_k(const void* dy, const void* ys, const int32_t* pos
   constexpr int kTok = kRowThreads / 64;
   const int64_t tb = (tokens + kTok - 1) / kTok, zb = (rows + kZeroRows - 1) / kZeroRows;
   if (tb + zb == 0) return hipSuccess;
-  hipLaunchKernelGGL((k_expert_combine_backward<T, K>), dim3((unsigned)(tb + zb)),
+  hipLaunchKernelGGL((k_expert_combine_backward<T, K>), row_grid(tb + zb),
                      dim3(kRowThreads), 0, s, static_cast<const T*>(dy),
                      static_cast<const T*>(ys), pos, src, weights, tokens, (uint32_t)topk, rows,
                      (uint32_t)dim, nvec, (uint32_t)tb, static_cast<T*>(dys), dweights);

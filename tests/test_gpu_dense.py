@@ -799,3 +799,40 @@ def test_clip_of_more_chunks_than_blocks():
     same = [x.clone() for x in grads]
     run_clip(same[:1], [torch.float32], 1e9, in_place=True)
     assert torch.equal(same[0], grads[0]) and all(torch.equal(a, b) for a, b in zip(want, outs))
+
+
+def test_expert_rows_beyond_32_bit_offsets_and_one_grid_line():
+    """33.6 million tokens of 512 x bf16: element offsets pass 2^34, and the row kernels take
+    more blocks than one line of a grid holds.  Every row is checked, bit for bit."""
+    n, dim, chunk = 33_600_000, 512, 1 << 16
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of free device memory")
+    i32 = dict(dtype=torch.int32, device=DEV)
+    base = torch.randint(0, 0x3F80, (chunk, dim), generator=gen(2), dtype=torch.int16, device=DEV)
+    x = torch.empty(n, dim, dtype=torch.bfloat16, device=DEV)
+
+    def rows_of(c):
+        return (base + c)[:min(chunk, n - c * chunk)]  # 0x3F80 + 513: still finite
+    for c in range(-(-n // chunk)):
+        x[c * chunk:(c + 1) * chunk] = rows_of(c).view(torch.bfloat16)
+    ids = torch.randint(0, 3, (n, 1), generator=gen(3), device=DEV)
+    off, src, pos = torch.empty(4, **i32), torch.empty(n, **i32), torch.empty(n, 1, **i32)
+    need = eb.emb_expert_workspace_bytes(n, 1, 3)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    eb.check(eb.emb_expert_sort(ids, n, 1, 3, 0, off, src, pos, ws, need), "sort")
+    order = torch.argsort(ids.view(-1), stable=True)
+    assert torch.equal(src, order.int())
+    assert torch.equal(pos.view(-1)[order], torch.arange(n, **i32))
+    del order, ids
+    a = (n, 1, n, dim, eb.EMB_BF16)
+    xs = torch.full_like(x, 7)
+    eb.check(eb.emb_expert_dispatch(x, pos, src, *a, xs), "dispatch")
+    for c in range(-(-n // chunk)):
+        got = xs[pos[c * chunk:(c + 1) * chunk, 0].long()]
+        assert torch.equal(got.view(torch.int16), rows_of(c)), c
+    x.fill_(7)
+    eb.check(eb.emb_expert_combine(xs, pos, None, *a, x), "combine")
+    for c in range(-(-n // chunk)):
+        assert torch.equal(x[c * chunk:(c + 1) * chunk].view(torch.int16), rows_of(c)), c
+    del x, xs
+    torch.cuda.empty_cache()
