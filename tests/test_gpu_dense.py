@@ -836,3 +836,42 @@ def test_expert_rows_beyond_32_bit_offsets_and_one_grid_line():
         assert torch.equal(x[c * chunk:(c + 1) * chunk].view(torch.int16), rows_of(c)), c
     del x, xs
     torch.cuda.empty_cache()
+
+
+def test_wide_rows_and_long_lists_in_a_graph():
+    """Rows whose weights pass 64 KB of LDS, and a list of several launches, captured and
+    replayed beside eager work: the eager bits each time."""
+    n, dim = 37, 6000
+    x, block, gt, w_post, scale, w_pre, dy, dh = norm_inputs(8, n, dim, torch.float32, "element",
+                                                             True)
+    y, h, dx, db, dg = (torch.zeros_like(x) for _ in range(5))
+    sums = torch.zeros(3, dim, device=DEV)
+    grads = [rand(gen(9), 50 + i) for i in range(250)]
+    outs = [torch.zeros_like(v) for v in grads]
+    gl, ol, norm = eb.TensorList(grads), eb.TensorList(outs), torch.zeros(2, device=DEV)
+    need = max(eb.emb_gated_norm_workspace_bytes(n, dim), eb.emb_grad_workspace_bytes(gl))
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV).fill_(255)
+    code = eb.EMB_GATE_ELEMENT | eb.EMB_GATE_SIGMOID
+
+    def run():
+        eb.check(eb.emb_gated_norm_forward(x, block, gt, w_post, scale, w_pre, n, dim, eb.EMB_F32,
+                                           code, 1e-6, y, h), "forward")
+        eb.check(eb.emb_gated_norm_backward(y, block, gt, w_post, scale, w_pre, dy, dh, n, dim,
+                                            eb.EMB_F32, code, 1e-6, dx, db, dg, *sums, ws, need),
+                 "backward")
+        eb.check(eb.emb_clip_grad_norm(gl, ol, None, 0, 0.5, norm, ws, need), "clip")
+    results_ = [y, h, dx, db, dg, sums, norm] + outs
+    run()
+    torch.cuda.synchronize()
+    want = [v.clone() for v in results_]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        run()
+    for r in range(3):
+        for v in results_:
+            v.zero_()
+        graph.replay()
+        scratch = torch.randn(1 << 20, device=DEV).sum()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(results_, want)), f"replay {r}"
+        del scratch
