@@ -53,14 +53,35 @@ constexpr int kMaxWaves = 16;
 constexpr int kCus = 256;
 constexpr int kForwardWaves = 14, kBackwardWaves = 8, kBackwardBlockRowWaves = 16;
 
-// 1 / (1 + 2^(-v log2 e)).  For 16-bit data the exponent is one product and the
-// quotient the hardware reciprocal (both within 2^-21 for |v| < 8, far below
-// the data's own rounding); infinite gates give 0 and 1, a NaN stays one.
-// fp32 takes the library's exponential.
+// e^-v.  For 16-bit data one product and the hardware exponential, within
+// (1.5 |v| + 2) * 2^-24 and so far below the data's own rounding up to |v| = 87,
+// where it is 0 or infinite; fp32 takes the library's exponential.
 template <class T>
-__device__ inline float sigmoid(float v) {
-  if constexpr (sizeof(T) == 4) return 1.0f / (1.0f + expf(-v));
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896340736f));
+__device__ inline float exp_neg(float v) {
+  if constexpr (sizeof(T) == 4) return expf(-v);
+  return __builtin_amdgcn_exp2f(v * -1.44269504088896340736f);
+}
+
+// a (1 - a) for a = 1 / (1 + t), t = e^-v.  1 - a cancels where a is near 1 (in
+// fp32 one percent is lost at v = 12, all of it at 17), so an open gate takes it
+// as t a.
+__device__ inline float sigmoid_slope(float v, float t, float a) {
+  return a * (v > 0.0f ? t * a : 1.0f - a);
+}
+
+// A gate's factor: a = v, or 1 / (1 + e^-v) (for 16-bit data with the hardware
+// reciprocal; infinite gates give 0 and 1, a NaN stays one), and da/dv.
+struct Factor {
+  float a, slope;
+};
+template <class T>
+__device__ inline Factor gate_factor(float v, bool sig) {
+  if (!sig) return {v, 1.0f};
+  const float t = exp_neg<T>(v);
+  float a;
+  if constexpr (sizeof(T) == 4) a = 1.0f / (1.0f + t);
+  else a = __builtin_amdgcn_rcpf(1.0f + t);
+  return {a, sigmoid_slope(v, t, a)};
 }
 
 // 1 / sqrt(x) by the hardware instruction (1 ulp), which takes no denormals:
@@ -230,7 +251,7 @@ __device__ inline void place_weights(Weights<T, V, MULTI> (&w)[3]) {
 template <class T, int V, int S>
 struct RowData {
   Raw<T> in[S][V], gate[V];
-  float a;
+  float row_gate;
 
   template <bool TAIL>
   __device__ inline void load(const T* const (&p)[S], const T* g, int32_t gate_kind, int64_t r,
@@ -243,24 +264,22 @@ struct RowData {
       if (gate_kind == EMB_GATE_ELEMENT)
         gate[v] = load_raw<T, kVec<T>, true>(g + at + c.col[v]);
     }
-    a = gate_kind == EMB_GATE_ROW ? to_f32(g[r]) : 1.0f;
+    row_gate = gate_kind == EMB_GATE_ROW ? to_f32(g[r]) : 1.0f;
   }
 
-  // The gate's factors; a becomes the row's.
-  __device__ inline void factors(int32_t gate_kind, bool sig, float (&out)[V][kVec<T>]) {
-    if (gate_kind == EMB_GATE_ELEMENT) {
+  // The gate's factors and slopes (those of a row gate in every place).
+  __device__ inline void factors(int32_t gate_kind, bool sig, float (&a)[V][kVec<T>],
+                                 float (&slope)[V][kVec<T>]) const {
+    const Factor row = gate_factor<T>(row_gate, sig && gate_kind == EMB_GATE_ROW);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int e = 0; e < kVec<T>; ++e)
-          out[v][e] = sig ? sigmoid<T>(gate[v].get(e)) : gate[v].get(e);
-    } else {
-      if (sig) a = sigmoid<T>(a);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) out[v][e] = a;
-    }
+      for (int e = 0; e < kVec<T>; ++e) {
+        const Factor f =
+            gate_kind == EMB_GATE_ELEMENT ? gate_factor<T>(gate[v].get(e), sig) : row;
+        a[v][e] = f.a;
+        slope[v][e] = f.slope;
+      }
   }
 };
 
@@ -292,8 +311,8 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void k_gated_norm_forward(
   clear_sums<MULTI>(lds);
   // every thread of a block takes the same number of rounds (barriers)
   for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < rows; r0 += step, r += step) {
-    float a[V][N];
-    cur.factors(gate_kind, sig, a);
+    float a[V][N], slope[V][N];
+    cur.factors(gate_kind, sig, a, slope);
     float ro_s = 1.0f;
     if (w_post) {
       float s[1] = {0.0f};
@@ -359,6 +378,10 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void k_gated_norm_backward(
     T* dblock, T* dgate, float* __restrict__ parts) {
   constexpr int N = kVec<T>;
   enum { Y = 0, O = 1, DH = 2, DY = 3 };
+  // The slopes of an element gate stay in registers from the factors on; the
+  // fp32 blocks of up to 1024 threads have none left (41 spilled, 8000 columns
+  // 235 us against 220) and form them again where they are used.
+  constexpr bool kHeld = !(MULTI && sizeof(T) == 4);
   __shared__ SumBuffers lds;
   uint32_t turn = 0;
   const uint32_t lane = MULTI ? threadIdx.x : threadIdx.x % (uint32_t)tpr;
@@ -384,8 +407,8 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void k_gated_norm_backward(
   clear_sums<MULTI>(lds);
   for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < rows; r0 += step, r += step) {
     const bool live = r < rows;
-    float a[V][N];
-    cur.factors(gate_kind, sig, a);
+    float a[V][N], slope[V][N];
+    cur.factors(gate_kind, sig, a, slope);
     // sums of y^2, q * y and o^2
     float s1[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -457,18 +480,24 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void k_gated_norm_backward(
             const float ohat = cur.in[O][v].get(e) * ro_s, ts = tv[v][e] * sc[i];
             const float p = (ts * a[v][e]) * wpost[i], da = ts * (ohat * wpost[i]);
             ov[e] = w_post ? ro_s * (p - ohat * mp) : p;
-            gv[e] = sig ? da * (a[v][e] * (1.0f - a[v][e])) : da;
+            gv[e] = kHeld ? da * slope[v][e] : da;
           }
         }
         o.set_all(ov);
         store_raw<T, N, true>(dblock + at + c.col[v], o);
         if (gate_kind == EMB_GATE_ELEMENT) {
+          if (!kHeld && sig)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              const float g = cur.gate[v].get(e);
+              gv[e] *= sigmoid_slope(g, exp_neg<T>(g), a[v][e]);
+            }
           o.set_all(gv);
           store_raw<T, N, true>(dgate + at + c.col[v], o);
         }
       }
       if (gate_kind == EMB_GATE_ROW && lane == 0)
-        dgate[r] = from_f32<T>(sig ? s2[1] * (cur.a * (1.0f - cur.a)) : s2[1]);
+        dgate[r] = from_f32<T>(s2[1] * gate_factor<T>(cur.row_gate, sig).slope);
     }
     if (r0 + step < rows)
       cur.load(in, gate, gate_kind, r + step < last ? r + step : last, dim, c);

@@ -875,3 +875,43 @@ def test_wide_rows_and_long_lists_in_a_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(results_, want)), f"replay {r}"
         del scratch
+
+
+# ---------------------------------------------------------------- open and shut gates
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("gate", ["row", "element"])
+@pytest.mark.parametrize("dim", [40, 512, 1664])
+def test_gate_gradient_near_saturation(kind, gate, dim):
+    """The gradient of a sigmoid gate keeps its digits where the gate is nearly open or shut.
+    Without a norm before the gate and with dh = 0 it is a (1 - a) times the product dy * block
+    (summed over the row for a row gate), all of whose terms are positive here."""
+    t, g = TYPES[kind], gen(dim)
+    v = torch.cat([torch.linspace(6, 20, 113, device=DEV), torch.linspace(-20, -6, 113, device=DEV),
+                   torch.linspace(-6, 6, 31, device=DEV)]).to(t)
+    n = v.numel()
+    each = 120.0 if gate == "element" else 120.0 / dim ** 0.5  # products in the range of fp16
+    block, dy = ((each * (1 + torch.rand(n, dim, generator=g, device=DEV))).to(t)
+                 for _ in range(2))
+    gt = v if gate == "row" else v[:, None].expand(n, dim).contiguous()
+    y, dh, one = rand(g, n, dim).to(t), torch.zeros_like(block), torch.ones(dim, device=DEV)
+    dx, db, dg = torch.empty_like(y), torch.empty_like(y), torch.empty_like(gt)
+    sums = torch.empty(2, dim, device=DEV)
+    need = eb.emb_gated_norm_workspace_bytes(n, dim)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV).fill_(255)
+    eb.check(eb.emb_gated_norm_backward(y, block, gt, None, one, one, dy, dh, n, dim,
+                                        eb.dtype_code(t), gate_code(gate, True), 1e-6, dx, db, dg,
+                                        None, *sums, ws, need), "backward")
+    torch.cuda.synchronize()
+    assert torch.equal(dx, dy)
+    vd = v.double()[:, None]
+    f = torch.sigmoid(vd) * torch.sigmoid(-vd)
+    da = dy.double() * block.double()
+    # e^-v: 1.5 |v| + 2 steps (the exponent's product and the result); the sigmoid: as much and
+    # 3 (sum, reciprocal); the factor takes it twice and two products, the gradient one more,
+    # and a row's sum its own
+    rel = 3 * vd.abs() + 14 + (1 if gate == "element" else 3 + sum_steps(dim, t))
+    if gate == "row":
+        da = da.sum(1, keepdim=True)
+    ref = (f * da).reshape(gt.shape)
+    within(dg, ref, (rel * U * (f * da)).reshape(gt.shape), "dgate")
