@@ -3,6 +3,7 @@
 #pragma once
 
 #include "embtab_internal.hpp"
+#include "grid.hpp"
 
 namespace embtab {
 
@@ -110,6 +111,14 @@ __device__ inline void store_raw(T* p, const Raw<T, N>& r) {
     else *q = x;
   }
 }
+
+// Blocks of a kernel of 256 threads a block, which finds its index with
+// block_index().
+inline dim3 row_grid(int64_t blocks) {
+  const Grid g = fold_grid(blocks);
+  return dim3(g.x, g.y);
+}
+__device__ inline uint32_t block_index() { return blockIdx.y * gridDim.x + blockIdx.x; }
 
 inline bool dtype_ok(int32_t t) { return t == EMB_F32 || t == EMB_BF16 || t == EMB_F16; }
 inline size_t dtype_size(int32_t t) { return t == EMB_F32 ? 4 : 2; }

@@ -215,16 +215,6 @@ __device__ inline uint32_t vec_column(uint32_t v, uint32_t dim) {
 
 constexpr int kRowThreads = 256;
 
-// A launch holds fewer than 2^32 threads along x: more blocks of the row
-// kernels than that go along y too.  Block indexes past the last one find no
-// token and no row.
-constexpr int64_t kGridX = 1 << 23;
-__device__ inline uint32_t block_index() { return blockIdx.y * gridDim.x + blockIdx.x; }
-dim3 row_grid(int64_t blocks) {
-  return blocks <= kGridX ? dim3((unsigned)blocks)
-                          : dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
-}
-
 constexpr int kRowVecs = 4;          // vectors in flight per thread
 constexpr uint32_t kWideVecs = 64;   // vectors of a row that takes a wave of its own
 constexpr uint32_t kZeroRows = 64;   // rows checked by one zero-fill block

@@ -288,7 +288,9 @@ __global__ __launch_bounds__(1024) void k_sum_doubles(const double* __restrict__
   out[0] = t;
 }
 
-// One sub-group per distinct row.  The square root and the reciprocal are the
+// One sub-group per distinct row; up to 2^32 - 1 rows, so the blocks past kGridX
+// go along y (a block index times the rows of a block stays below 2^32 there:
+// 2^32 / rows is a multiple of kGridX).  The square root and the reciprocal are the
 // hardware instructions (each within 1 ulp), as in the fused step.
 template <int SG, int VEC>
 __global__ __launch_bounds__(256) void k_adagrad_rows(
@@ -296,7 +298,7 @@ __global__ __launch_bounds__(256) void k_adagrad_rows(
     const uint32_t* __restrict__ misc, const float* __restrict__ sums,
     const float* __restrict__ scale, float* __restrict__ W, float* __restrict__ G,
     uint32_t most, uint32_t sentinel, int32_t D, float lr, float eps) {
-  const uint32_t u = blockIdx.x * (256 / SG) + threadIdx.x / SG;
+  const uint32_t u = block_index() * (256 / SG) + threadIdx.x / SG;
   const float s = scale ? scale[0] : 1.0f;
   if (s == 0.0f || u >= most || u >= misc[kMiscNumUnique]) return;
   const uint32_t lane = threadIdx.x % SG, D4 = (uint32_t)D >> 2;
@@ -362,8 +364,8 @@ hipError_t step_t(const Handle& h, const Plan& p, const uint32_t* keys, const fl
                   const float* scale, float lr, float eps, char* ws, hipStream_t s) {
   const int64_t most = p.nnz < h.total_rows ? p.nnz : h.total_rows;
   constexpr int kRows = 256 / SG;
-  hipLaunchKernelGGL((k_adagrad_rows<SG, VEC>), dim3((unsigned)((most + kRows - 1) / kRows)),
-                     dim3(256), 0, s, keys, reinterpret_cast<const uint32_t*>(ws + p.seg_off),
+  hipLaunchKernelGGL((k_adagrad_rows<SG, VEC>), row_grid((most + kRows - 1) / kRows), dim3(256),
+                     0, s, keys, reinterpret_cast<const uint32_t*>(ws + p.seg_off),
                      reinterpret_cast<const uint32_t*>(ws + p.misc), sums, scale, h.W, h.G,
                      (uint32_t)most, (uint32_t)h.total_rows, h.D, lr, eps);
   return hipGetLastError();

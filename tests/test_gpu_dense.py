@@ -915,3 +915,53 @@ def test_gate_gradient_near_saturation(kind, gate, dim):
         da = da.sum(1, keepdim=True)
     ref = (f * da).reshape(gt.shape)
     within(dg, ref, (rel * U * (f * da)).reshape(gt.shape), "dgate")
+
+
+# ---------------------------------------------------------------- tables of many rows
+
+def test_row_step_of_more_rows_than_one_grid_line():
+    """2^26 + 1 distinct rows of 132 floats, four to a block: more threads than a launch holds
+    along x.  Every row is checked."""
+    rows, D, B, lr, eps, c = (1 << 26) + 1, 132, 64, 0.05, 1e-6, 0.37
+    if torch.cuda.mem_get_info()[0] < 130 << 30:
+        pytest.skip("needs 130 GB of free device memory")
+    tabs = eb.EmbTables([rows], D)
+    tabs.weights.fill_(0.5)
+    tabs.accum.fill_(0.25)
+    grad = rand(gen(6), B, 1, D)
+    each = -(-rows // B)
+    offsets = torch.clamp(torch.arange(B + 1, device=DEV) * each, max=rows)
+    ids = torch.arange(rows - 1, -1, -1, device=DEV)  # occurrence j is row rows - 1 - j
+    ws, need = tabs.workspace(B, rows)
+    sums = torch.empty(rows, D, device=DEV)
+    sq, scale = torch.empty(1, dtype=torch.float64, device=DEV), torch.tensor([c], device=DEV)
+    eb.check(eb.emb_bag_prepare(tabs.handle, offsets, ids, B, rows, 0, ws, need), "prepare")
+    del ids
+    eb.check(eb.emb_bag_grad_reduce_prepared(tabs.handle, B, rows, 0, grad, sums, sq, ws, need),
+             "reduce")
+    eb.check(eb.emb_bag_adagrad_reduced_prepared(tabs.handle, B, rows, sums, scale, lr, eps, ws,
+                                                 need), "step")
+    torch.cuda.synchronize()
+    g = grad[:, 0].double()
+    lens = (offsets[1:] - offsets[:-1]).double()
+    want = float(((g * g).sum(1) * lens).sum())
+    assert abs(float(sq) - want) <= 1e-12 * want  # one term a row, summed in 64 bits
+    f = float(scale[0]) * g
+    G = 0.25 + f * f
+    W = 0.5 - lr * f / (G.sqrt() + eps)
+    # the library's rule: 1e-5 of the terms plus 1e-6
+    eG = 1e-5 * (0.25 + f * f) + 1e-6
+    eW = 1e-5 * (0.5 + lr * f.abs() / (G.sqrt() + eps)) + 1e-6
+    per = [(v - e).float() for v, e in ((W, eW), (G, eG))], \
+        [(v + e).float() for v, e in ((W, eW), (G, eG))]
+    chunk = 1 << 20
+    for at in range(0, rows, chunk):
+        r = torch.arange(at, min(at + chunk, rows), device=DEV)
+        bag = (rows - 1 - r) // each
+        for k, have in enumerate((tabs.weights, tabs.accum)):
+            v = have[at:at + chunk]
+            assert ((v >= per[0][k][bag]) & (v <= per[1][k][bag])).all(), (k, at)
+        assert torch.equal(sums[at:at + chunk], grad[bag, 0]), at
+    tabs.close()
+    del tabs, sums, ws
+    torch.cuda.empty_cache()
