@@ -568,12 +568,14 @@ def dtype_code(dtype) -> int:
 
 class TensorList:
     """The HOST array of emb_tensor_t that emb_clip_grad_norm takes, over contiguous torch
-    tensors, which it keeps alive.  Made once for the buffers a program keeps."""
+    tensors of one GPU, which it keeps alive.  Made once for the buffers a program keeps."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
         self.array = (emb_tensor_t * max(1, len(self.tensors)))()
         for item, t in zip(self.array, self.tensors):
+            if t.device.type != "cuda" or t.device != self.tensors[0].device:
+                raise ValueError(f"a tensor on {t.device}: all on one GPU are wanted")
             if not t.is_contiguous():
                 raise ValueError(f"a tensor of shape {tuple(t.shape)} is not contiguous")
             item.data, item.numel, item.dtype = t.data_ptr(), t.numel(), dtype_code(t.dtype)

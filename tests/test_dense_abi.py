@@ -163,3 +163,39 @@ def test_gated_norm_refusals():
     for kw in (dict(ws=None), dict(ws=A + 16), dict(wb=need - 1)):
         assert bwd(**kw) == WS, kw
     assert fwd(n=0, x=None, block=None, gate=None, y=None, h=None) == eb.EMB_OK
+
+
+class FakeTensor:
+    """What TensorList reads of a tensor, on any device."""
+
+    def __init__(self, device, shape=(4,), dtype="torch.float32", contiguous=True):
+        import torch
+        self.device, self.shape, self.dtype = torch.device(device), shape, dtype
+        self.contiguous = contiguous
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def data_ptr(self):
+        return A
+
+    def numel(self):
+        return 4
+
+
+def test_tensor_list_takes_tensors_of_one_gpu():
+    import torch
+    with pytest.raises(ValueError, match="cpu"):
+        eb.TensorList([torch.zeros(4)])
+    with pytest.raises(ValueError, match="meta"):
+        eb.TensorList([torch.zeros(4, device="meta")])
+    good = eb.TensorList([FakeTensor("cuda:1"), FakeTensor("cuda:1", dtype="torch.bfloat16")])
+    assert [(a.data, a.numel, a.dtype) for a in good.array] == [(A, 4, 0), (A, 4, 1)]
+    for bad in ([FakeTensor("cuda:0"), FakeTensor("cuda:1")],
+                [FakeTensor("cuda:0"), FakeTensor("cpu")], [FakeTensor("cpu"), FakeTensor("cpu")]):
+        with pytest.raises(ValueError, match="one GPU"):
+            eb.TensorList(bad)
+    for bad in (FakeTensor("cuda:0", contiguous=False),
+                FakeTensor("cuda:0", dtype="torch.float64")):
+        with pytest.raises(ValueError):
+            eb.TensorList([bad])
