@@ -31,6 +31,15 @@ constexpr int kClipItems = 104;     // 36 bytes each: the arguments stay under 4
 constexpr int kClipParts = 1024;    // blocks (and partial sums) of one sum launch
 constexpr int kScaleBlocks = 2048;  // blocks of one scale launch: what the chip holds
 
+// The sums (partial ones and the caller's) are added by every block of every
+// scale launch up to this many times the launches; beyond, one block adds them
+// first, or the work would grow with the square of the list's length.  10000
+// tensors of 81920 fp32 elements, 97 launches and 97 thousand sums: 2.26 ms,
+// and 7.1 added by every block; 2500 tensors 0.56 and 0.82; 200 tensors (4
+// thousand sums times launches) 43 us either way; 12 small tensors and 3000
+// sums of the caller's 17 and 14.
+constexpr int64_t kClipDirect = 4 * kClipParts;
+
 struct ClipItem {
   const void* in;
   void* out;
@@ -128,14 +137,26 @@ __global__ __launch_bounds__(kClipThreads) void k_grad_square_sum(const ClipList
   if (threadIdx.x == 0) parts[blockIdx.x] = acc;
 }
 
+// This thread's share of n values, added one after another with eight loads in
+// flight.
+__device__ inline double strided_sum(double acc, const double* __restrict__ v, uint32_t n) {
+  for (uint32_t i = threadIdx.x; i < n; i += 8u * kClipThreads) {
+    double x[8];
+#pragma unroll
+    for (uint32_t k = 0; k < 8u; ++k)
+      x[k] = n - i > k * kClipThreads ? v[i + k * kClipThreads] : 0.0;
+#pragma unroll
+    for (uint32_t k = 0; k < 8u; ++k) acc += x[k];
+  }
+  return acc;
+}
+
 // The norm and the coefficient from the partial sums, the same in every thread
 // of every block that forms them.
 __device__ inline float2 norm_and_coef(const double* __restrict__ parts, uint32_t num_parts,
                                        const double* __restrict__ extra, int32_t num_extra,
                                        float max_norm, double* lds4) {
-  double acc = 0.0;
-  for (uint32_t i = threadIdx.x; i < num_parts; i += kClipThreads) acc += parts[i];
-  for (int32_t i = threadIdx.x; i < num_extra; i += kClipThreads) acc += extra[i];
+  const double acc = strided_sum(strided_sum(0.0, parts, num_parts), extra, (uint32_t)num_extra);
   const double norm = sqrt(block_sum(acc, lds4));
   double c = (double)max_norm / (norm + 1e-6);
   c = c < 1.0 ? c : 1.0;
@@ -188,17 +209,33 @@ __device__ inline void scale_item(const ClipItem& it, int64_t at, int64_t len, f
   }
 }
 
-// Every block forms the coefficient itself (at most a few thousand sums, which
-// its L2 holds), so no launch stands between the sum and the scale; the first
-// block of the first launch stores it.  The chunks go from the last one back:
-// what the sum read last is still in the cache.
+__global__ __launch_bounds__(kClipThreads) void k_clip_norm(const double* __restrict__ parts,
+                                                            uint32_t num_parts,
+                                                            const double* __restrict__ extra,
+                                                            int32_t num_extra, float max_norm,
+                                                            float* __restrict__ norm_out) {
+  __shared__ double lds4[4];
+  const float2 nc = norm_and_coef(parts, num_parts, extra, num_extra, max_norm, lds4);
+  if (threadIdx.x == 0) {
+    norm_out[0] = nc.x;
+    norm_out[1] = nc.y;
+  }
+}
+
+// Every block forms the coefficient itself (at most kClipDirect sums, which its
+// L2 holds), so no launch stands between the sum and the scale, and the first
+// block of the first launch stores it; for longer lists it is `ready`.  The
+// chunks go from the last one back: what the sum read last is still in the
+// cache.
 __global__ __launch_bounds__(kClipThreads) void k_clip_scale(
     const ClipList l, const double* __restrict__ parts, uint32_t num_parts,
     const double* __restrict__ extra, int32_t num_extra, float max_norm,
-    float* __restrict__ norm_out) {
+    const float* __restrict__ ready, float* __restrict__ norm_out) {
   __shared__ double lds4[4];
   const ClipFinder find(l);
-  const float2 nc = norm_and_coef(parts, num_parts, extra, num_extra, max_norm, lds4);
+  float2 nc = make_float2(0.0f, 0.0f);
+  if (ready) nc.y = *ready;
+  else nc = norm_and_coef(parts, num_parts, extra, num_extra, max_norm, lds4);
   const float c = nc.y;
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) {
     norm_out[0] = nc.x;
@@ -258,21 +295,28 @@ hipError_t launch_clip_grad_norm(const emb_tensor_t* grads, const emb_tensor_t* 
   double* parts = reinterpret_cast<double*>(ws);
   ClipList l;
   int32_t at = 0;
-  uint32_t num_parts = 0;
+  uint32_t num_parts = 0, launches = 0;
   while (next_list(grads, out, n, &at, &l)) {
     const unsigned grid = sum_blocks(l);
     hipLaunchKernelGGL(k_grad_square_sum, dim3(grid), dim3(kClipThreads), 0, s, l,
                        parts + num_parts);
     num_parts += grid;
+    ++launches;
   }
+  // (without an output one block forms the coefficient in any case)
+  const bool direct = !out || ((int64_t)num_parts + num_extra) * launches <= kClipDirect;
+  if (!direct)
+    hipLaunchKernelGGL(k_clip_norm, dim3(1), dim3(kClipThreads), 0, s, parts, num_parts, extra,
+                       num_extra, max_norm, norm_out);
   // the coefficient is wanted without an output too: then of an empty list
   at = out ? 0 : n;
   bool more = next_list(grads, out, n, &at, &l);
-  float* store = norm_out;
+  const float* ready = direct ? nullptr : norm_out + 1;
+  float* store = direct ? norm_out : nullptr;
   do {
     const unsigned grid = l.chunks < (unsigned)kScaleBlocks ? l.chunks : (unsigned)kScaleBlocks;
     hipLaunchKernelGGL(k_clip_scale, dim3(grid ? grid : 1u), dim3(kClipThreads), 0, s, l, parts,
-                       num_parts, extra, num_extra, max_norm, store);
+                       num_parts, extra, num_extra, max_norm, ready, store);
     store = nullptr;
     more = more && next_list(grads, out, n, &at, &l);
   } while (more);

@@ -965,3 +965,63 @@ def test_row_step_of_more_rows_than_one_grid_line():
     tabs.close()
     del tabs, sums, ws
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------- long lists
+
+@pytest.mark.parametrize("count,num_extra", [(150, 5000), (2500, 0), (2500, 7), (12, 9000)])
+def test_clip_with_many_sums(count, num_extra):
+    """Lists whose sums one block adds before the scale, and the caller's many sums."""
+    g = gen(count + num_extra)
+    sizes = [[300_000, 9, 8193][i % 3] if count > 1000 else 8192 * 30 + i for i in range(count)]
+    flat = rand(g, sum(sizes), scale=0.1)
+    grads = [x.to(list(TYPES.values())[i % 3]) for i, x in enumerate(torch.split(flat, sizes))]
+    extra = torch.rand(num_extra, generator=g, device=DEV, dtype=torch.float64) \
+        if num_extra else None
+    sq = sum((x.double() ** 2).sum() for x in grads)
+    ref = (float(sq) + (float(extra.sum()) if num_extra else 0.0)) ** 0.5
+    coef = min(1.0, 1.0 / (ref + 1e-6))
+    norm, outs = run_clip(grads, [x.dtype for x in grads], 1.0, extra)
+    assert abs(float(norm[0]) - ref) <= 1.01 * U * ref
+    assert abs(float(norm[1]) - coef) <= 1.01 * U * coef
+    want = torch.cat([(x.double() * coef).float() for x in grads])  # rounded once more: U
+    got = torch.cat([o.float() for o in outs])
+    lim = torch.cat([torch.full((n,), half(x.dtype) + 4 * U, device=DEV, dtype=torch.float64)
+                     for n, x in zip(sizes, grads)]) * want.double().abs() + TINY[torch.float16]
+    assert ((got.double() - want.double()).abs() <= lim).all()
+    gl, alone = eb.TensorList(grads), torch.empty(2, device=DEV)
+    need = eb.emb_grad_workspace_bytes(gl)
+    eb.check(eb.emb_clip_grad_norm(gl, None, extra, num_extra, 1.0, alone,
+                                   torch.empty(need, dtype=torch.uint8, device=DEV), need), "norm")
+    assert torch.equal(alone, norm)
+    bad = torch.full((num_extra or 5000,), float("inf"), dtype=torch.float64, device=DEV)
+    norm, outs = run_clip(grads, [x.dtype for x in grads], 1.0, bad)
+    assert float(norm[1]) == 0.0 and all((o == 0).all() for o in outs[:50])
+
+
+def test_clip_time_does_not_grow_with_the_square_of_the_list():
+    """20000 tensors against one of the same elements.  The list takes 386 launches of its own
+    (about as long as reading the data); adding 200 thousand partial sums in every block of
+    every scale launch took ten times the data's time."""
+    count, each = 20_000, 81_920
+    flat = torch.ones(count * each, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(flat)
+
+    def best(split):
+        gl = eb.TensorList(flat.split(each) if split else [flat])
+        ol = eb.TensorList(out.split(each) if split else [out])
+        need = eb.emb_grad_workspace_bytes(gl)
+        ws, norm = torch.empty(need, dtype=torch.uint8, device=DEV), torch.empty(2, device=DEV)
+        times = []
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            eb.check(eb.emb_clip_grad_norm(gl, ol, None, 0, 1.0, norm, ws, need), "clip")
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        assert abs(float(norm[0]) - flat.numel() ** 0.5) <= 1.01 * U * flat.numel() ** 0.5
+        return min(times)
+
+    one, many = best(False), best(True)
+    assert many < 5 * one, (many, one)
