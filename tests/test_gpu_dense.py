@@ -7,7 +7,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import oracle as orc
 from recommender_embedding_tables_amd import synth
+from tests.helpers import StepBounds, abs_grad_sums
 
 pytestmark = pytest.mark.gpu
 
@@ -1025,3 +1027,112 @@ def test_clip_time_does_not_grow_with_the_square_of_the_list():
 
     one, many = best(False), best(True)
     assert many < 5 * one, (many, one)
+
+
+# ---------------------------------------------------------------- rounds over many rows
+
+# Short rows beyond what one round of the grid's blocks covers (768 blocks forward, 512 backward,
+# of 4 to 32 rows each), with a last round that not every group of lanes has a row for, and the
+# same of block-wide rows.
+ROUNDS = [(30_011, 40, "bf16"), (30_011, 40, "f32"), (20_005, 100, "f16"), (7_001, 512, "bf16"),
+          (7_001, 512, "f32"), (5_003, 479, "bf16"), (5_003, 479, "f32"), (1_501, 3328, "bf16"),
+          (1_103, 1001, "f32")]
+
+
+@pytest.mark.parametrize("gate,sig", [("row", True), ("element", True)])
+@pytest.mark.parametrize("n,dim,kind", ROUNDS)
+def test_gated_norm_in_rounds(n, dim, kind, gate, sig):
+    test_gated_norm(n, dim, kind, gate, sig, True)
+
+
+@pytest.mark.parametrize("gate,post", [("none", False), ("row", True), ("element", True)])
+@pytest.mark.parametrize("n,dim,kind", ROUNDS + [(3, 9, "f32"), (50, 24, "bf16"), (9, 5003, "f16")])
+def test_gated_norm_in_place(n, dim, kind, gate, post):
+    """y over x and dx over dy: the bits of separate outputs, also where a row's last vector
+    overlaps the one before and where groups without a row of the last round read along."""
+    t, code = TYPES[kind], gate_code(gate, True)
+    x, block, gt, w_post, scale, w_pre, dy, dh = norm_inputs(n + dim, n, dim, t, gate, post)
+    need = eb.emb_gated_norm_workspace_bytes(n, dim)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV).fill_(255)
+
+    def run(over):
+        x_, dy_ = x.clone(), dy.clone()
+        y = x_ if over else torch.empty_like(x)
+        dx = dy_ if over else torch.empty_like(dy)
+        h, db = torch.empty_like(x), torch.empty_like(x)
+        dg = None if gt is None else torch.empty_like(gt)
+        sums = torch.empty(3, dim, device=DEV)
+        dwp = sums[0] if post else None
+        eb.check(eb.emb_gated_norm_forward(x_, block, gt, w_post, scale, w_pre, n, dim,
+                                           eb.dtype_code(t), code, 1e-6, y, h), "forward")
+        eb.check(eb.emb_gated_norm_backward(y, block, gt, w_post, scale, w_pre, dy_, dh, n, dim,
+                                            eb.dtype_code(t), code, 1e-6, dx, db, dg, dwp,
+                                            sums[1], sums[2], ws, need), "backward")
+        torch.cuda.synchronize()
+        return [y, h, dx, db, sums[0 if post else 1:]] + ([] if dg is None else [dg])
+
+    apart = run(False)
+    for _ in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(run(True), apart))
+
+
+# ---------------------------------------------------------------- hashed tables
+
+def test_two_parts_on_hashed_tables():
+    """Rows found or inserted by key, stepped in two parts with the clip between them, over
+    batches that bring new rows and hold absent ids: the oracle's rows within the library's
+    per-step rule (1e-5 of a row's absolute terms, carried over the steps).  The gradients are
+    small enough that the clip's coefficient is 1 exactly."""
+    w = synth.workload(5, T=2, B=2000, universe=40_000, hash_capacity=1 << 16)
+    w.rows = np.full(w.T, int(0.625 * w.hash_capacity), np.int64)
+    kw = dict(hashed=True, seed=9, init_std=w.init_std, accum_init=w.accum_init)
+    tabs = eb.EmbTables(w.rows, w.D, hash_capacity=w.hash_capacity, **kw)
+    o = orc.Oracle(w.rows, w.D, **kw)
+    bounds = StepBounds(int(np.sum(w.rows)), w.D)
+    first = np.concatenate([[0], np.cumsum(w.rows)])
+    sq, norm = torch.empty(1, dtype=torch.float64, device=DEV), torch.empty(2, device=DEV)
+    none = eb.TensorList([])
+    clip_need = eb.emb_grad_workspace_bytes(none)
+    clip_ws = torch.empty(clip_need, dtype=torch.uint8, device=DEV)
+    known = np.zeros(0, np.int64)
+    for b in range(4):
+        offsets, ranks = synth.gen_batch(w, b)
+        keys, grad = synth.gen_keys(w, offsets, ranks), synth.gen_grad(w, b)
+        d_off, d_keys, nnz = t_(offsets), t_(keys.view(np.int64)), keys.size
+        ws, need = tabs.workspace(w.B, nnz)
+        d_ids = torch.empty(nnz, dtype=torch.int64, device=DEV)
+        eb.check(eb.emb_hash_find_or_insert(tabs.handle, d_off, d_keys, w.B, nnz, d_ids, ws, need),
+                 "find_or_insert")
+        ids, flags = o.find_or_insert(offsets, keys, w.B)
+        assert flags == 0 and np.array_equal(d_ids.cpu().numpy(), ids)
+        live = np.concatenate([np.arange(o.n_live(t)) + first[t] for t in range(w.T)])
+        bounds.assigned(o, np.setdiff1d(live, known))
+        known = live
+        ids[b::97] = eb.EMB_ID_ABSENT
+        d_ids = t_(ids)
+        sums = torch.empty(min(nnz, tabs.total_rows), w.D, device=DEV)
+        eb.check(eb.emb_bag_prepare(tabs.handle, d_off, d_ids, w.B, nnz, 0, ws, need), "prepare")
+        eb.check(eb.emb_bag_grad_reduce_prepared(tabs.handle, w.B, nnz, 0, t_(grad), sums, sq, ws,
+                                                 need), "reduce")
+        eb.check(eb.emb_clip_grad_norm(none, none, sq, 1, 1e9, norm, clip_ws, clip_need), "clip")
+        eb.check(eb.emb_bag_adagrad_reduced_prepared(tabs.handle, w.B, nnz, sums, norm[1:], w.lr,
+                                                     w.eps, ws, need), "step")
+        torch.cuda.synchronize()
+        # the sums against 64 bits, one rounding per added term, and the norm of them
+        uniq, s, a, cnt = plain_table_sums(list(w.rows), w.D, offsets, ids, w.B, False, grad)
+        bound, S = t_((cnt[:, None] + 2) * U * a), t_(s)
+        within(sums[:uniq.size], S, bound, "sums")
+        e = bound + U * S.abs()
+        lim = float((2 * S.abs() * e + e * e).sum()) + 1e-12 * float((S ** 2).sum())
+        assert abs(float(sq) - float((S ** 2).sum())) <= lim
+        assert float(norm[1]) == 1.0
+        rows, terms = abs_grad_sums(offsets, ids, w.B, o.rows, grad, False, w.D)
+        assert np.array_equal(rows, uniq)
+        assert bounds.step(o, rows, terms, w.lr, w.eps, lambda: o.backward_adagrad(
+            offsets, ids, w.B, False, grad, w.lr, w.eps)) == 0
+    rows = o.touched_rows()
+    W, G = o.read_rows(rows)
+    bounds.check(tabs.weights[t_(rows)].cpu().numpy(), tabs.accum[t_(rows)].cpu().numpy(), W, G,
+                 rows, "rows after the steps")
+    assert eb.emb_status_sync(tabs.handle) == (eb.EMB_OK, 0)
+    tabs.close()
