@@ -19,11 +19,12 @@
 // names no row is taken as dropped, so no access leaves the buffers.
 //
 // The row kernels are bound by memory (a one-shot device copy reaches 6.5 TB/s
-// here, rows written in scattered order 5.1 to 5.3).  They walk tokens, not rows: a token's row is read once and serves its
-// k choices from registers, where a walk over the rows would read it k times.
-// Outputs are stored past the caches, which they would only sweep: the forward
-// of 65536 tokens with two of 64 experts, 3328 x bf16, takes 490 us (5.3 TB/s)
-// against 520, the gradients of 16384 tokens with four 275 us (5.5 TB/s) against
+// here, rows written in scattered order 5.1 to 5.3).  They walk tokens, not
+// rows: a token's row is read once and serves its k choices from registers,
+// where a walk over the rows would read it k times.  Outputs are stored past the
+// caches, which they would only sweep: the forward of 65536 tokens with two of
+// 64 experts, 3328 x bf16, takes 490 us (5.3 TB/s) against 520, the gradients of
+// 16384 tokens with four 274 us of kernels (5.5 TB/s; 276 to 292 a pass) against
 // 313.
 #include "dense.hpp"
 

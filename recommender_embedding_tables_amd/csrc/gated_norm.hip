@@ -30,9 +30,10 @@
 // in block order: no atomics, the result does not depend on timing.
 //
 // Element-wise sigmoid gate, norm before the gate:
-//   forward   32768 x 3328 bf16   185 us, 5.9 TB/s (210 us where all five
+//   forward   32768 x 3328 bf16   182 us, 6.0 TB/s (210 us where all five
 //             streams begin at the same offset of a large power of two)
-//   backward  16384 x 3328 bf16   173 us, 5.0 TB/s, and 6 us for the column sums
+//   backward  16384 x 3328 bf16   167 to 178 us, 4.9 to 5.2 TB/s by the streams'
+//             places, 6 us of it the column sums
 // What moved them there: sums by lane permutations in place of LDS shuffles,
 // the hardware's exponential and reciprocal for 16-bit gates, weights in LDS.
 #include "dense.hpp"
@@ -44,12 +45,15 @@ namespace {
 typedef float fv4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxWaves = 16;
-// Waves a launch puts on each of the 256 CUs: few blocks that walk over many
-// rows each, so that the weights and column sums are set up once.  Measured on
-// 65536 x 512 bf16 rows: forward 61 us at 14 waves, 68 at 28; backward, whose
-// blocks leave 12 * dim bytes of sums each, 112 us at 8 waves, 122 at 16.  A
-// row that takes a whole block needs two blocks to hide its barriers (3328
-// columns: 7 waves each).
+// Waves a launch puts on each of the 256 CUs, in whole blocks and at least one:
+// few blocks that walk over many rows each, so that the weights and column sums
+// are set up once.  Measured on 65536 x 512 bf16 rows (blocks of 4 waves):
+// forward 61 us with 3 blocks, 68 with 7; backward, whose blocks leave 12 * dim
+// bytes of sums each, 112 us with 2, 122 with 4.  A row that takes a whole block
+// wants two blocks to hide its barriers, and has them up to 7 waves in the
+// forward, 8 in the backward; with one, 109 million bf16 values take 240 us
+// forward in rows of 4096 and 217 in rows of 6656, 183 with two in rows of 3584
+// (fp32: 202, 200 and 202).
 constexpr int kCus = 256;
 constexpr int kForwardWaves = 14, kBackwardWaves = 8, kBackwardBlockRowWaves = 16;
 

@@ -11,10 +11,10 @@
 // row written; the step then reads and writes rows of the distinct rows only,
 // where a second pass over the occurrences would gather every gradient row
 // again.  26 tables, D = 128, 1.7 million occurrences of 342 thousand rows: the
-// reduction 193 us (5.4 TB/s over its 1.05 GB), the step 158 us (5.5 TB/s).  The
-// sums are stored through the caches, where the step finds part of them again:
-// past them the step takes 174 us.  Eight gradient rows in flight per sub-group
-// instead of four change neither time.
+// reduction 194 us (5.5 TB/s over its 1.08 GB), the step 158 us (5.9 TB/s over
+// its 0.94 GB).  The sums are stored through the caches, where the step finds
+// part of them again: past them the step takes 174 us.  Eight gradient rows in
+// flight per sub-group instead of four change neither time.
 //
 // The sorted positions are cut into chunks, one sub-group of lanes each, and
 // blocks of chunks, as for the fused step.  A run inside a chunk is summed in
