@@ -36,7 +36,7 @@
 //             places, 6 us of it the column sums
 // What moved them there: sums by lane permutations in place of LDS shuffles,
 // the hardware's exponential and reciprocal for 16-bit gates, weights in LDS.
-#include "dense.hpp"
+#include "row_tiles.hpp"
 
 namespace embtab {
 
@@ -44,7 +44,6 @@ namespace {
 
 typedef float fv4 __attribute__((ext_vector_type(4)));
 
-constexpr int kMaxWaves = 16;
 // Waves a launch puts on each of the 256 CUs, in whole blocks and at least one:
 // few blocks that walk over many rows each, so that the weights and column sums
 // are set up once.  Measured on 65536 x 512 bf16 rows (blocks of 4 waves):
@@ -54,7 +53,6 @@ constexpr int kMaxWaves = 16;
 // forward, 8 in the backward; with one, 109 million bf16 values take 240 us
 // forward in rows of 4096 and 217 in rows of 6656, 183 with two in rows of 3584
 // (fp32: 202, 200 and 202).
-constexpr int kCus = 256;
 constexpr int kForwardWaves = 14, kBackwardWaves = 8, kBackwardBlockRowWaves = 16;
 
 // e^-v.  For 16-bit data one product and the hardware exponential, within
@@ -87,117 +85,6 @@ __device__ inline Factor gate_factor(float v, bool sig) {
   else a = __builtin_amdgcn_rcpf(1.0f + t);
   return {a, sigmoid_slope(v, t, a)};
 }
-
-// 1 / sqrt(x) by the hardware instruction (1 ulp), which takes no denormals:
-// those are scaled up by 2^64 first.
-__device__ inline float inv_sqrt(float x) {
-  const bool tiny = x < 0x1p-100f;
-  return __builtin_amdgcn_rsqf(tiny ? x * 0x1p64f : x) * (tiny ? 0x1p32f : 1.0f);
-}
-
-// How the rows lie on the threads: tpr threads share a row (8 .. 64 lanes of
-// a wave, or, MULTI, the whole block), each holding V vectors of it, at most 8
-// values: the backward pass holds about 15 registers for each.
-struct Shape {
-  int32_t tpr, threads, vecs, multi;
-  int32_t rows_per_block() const { return multi ? 1 : threads / tpr; }
-  int32_t waves() const { return threads / 64; }
-};
-
-template <class T>
-Shape shape_of(int32_t dim) {
-  const int nvec = (dim + kVec<T> - 1) / kVec<T>;
-  Shape s{8, 256, 1, 0};
-  while (s.tpr < 64 && s.tpr < nvec) s.tpr *= 2;
-  if (nvec <= 64) return s;
-  s.vecs = sizeof(T) == 4 ? 2 : 1;
-  if (nvec <= 64 * s.vecs) return s;
-  s.multi = 1;
-  s.tpr = s.threads = ((nvec + s.vecs - 1) / s.vecs + 63) / 64 * 64;
-  return s;
-}
-
-template <int CTRL>
-__device__ inline float dpp(float v) {
-  return __uint_as_float(
-      (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
-}
-
-// Sum over groups of tpr (8, 16, 32 or 64) neighbouring lanes, in every lane:
-// quads, half rows and rows by lane permutations, then pairs of rows and the
-// halves of the wave by row swaps; no LDS.  Both lanes of a pair add the same
-// two values, so the lanes' results have the same bits.
-__device__ inline float lanes_sum(float v, int tpr) {
-  v += dpp<0xB1>(v);   // quad_perm 1,0,3,2
-  v += dpp<0x4E>(v);   // quad_perm 2,3,0,1
-  v += dpp<0x141>(v);  // the other quad of 8
-  if (tpr >= 16) v += dpp<0x140>(v);  // the other half of 16
-  if (tpr >= 32) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
-                                                    false);
-    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-  if (tpr >= 64) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
-                                                    false);
-    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-  return v;
-}
-
-// Sums of N values over the threads of a row.  MULTI rows pass through LDS,
-// with one barrier: the calls of a kernel alternate between two buffers, so a
-// wave that writes for the next sum never meets one that still reads this
-// one.  Lane l then takes wave l % 16's part (zero for a wave the block does
-// not have) and the 16 are added as above.
-struct SumBuffers {
-  float part[2][3][kMaxWaves];
-};
-
-template <bool MULTI, int N>
-__device__ inline void row_sum(float (&v)[N], int tpr, SumBuffers& lds, uint32_t& turn) {
-#pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = lanes_sum(v[k], MULTI ? 64 : tpr);
-  if (!MULTI) return;
-  float(*part)[kMaxWaves] = lds.part[turn];
-  turn ^= 1u;
-  if ((threadIdx.x & 63u) == 0u)
-#pragma unroll
-    for (int k = 0; k < N; ++k) part[k][threadIdx.x >> 6] = v[k];
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = lanes_sum(part[k][threadIdx.x % kMaxWaves], kMaxWaves);
-}
-
-template <bool MULTI>
-__device__ inline void clear_sums(SumBuffers& lds) {
-  if (!MULTI) return;
-  for (uint32_t i = threadIdx.x; i < 2u * 3u * kMaxWaves; i += blockDim.x)
-    (&lds.part[0][0][0])[i] = 0.0f;
-  __syncthreads();
-}
-
-// The columns of one thread: vector v starts at col[v].  A vector that would
-// pass the row's end is moved back to end with it (TAIL: the width is not a
-// multiple of the vector); its elements before skip[v] belong to the vector
-// before and are left out of sums, and stored twice with the same value.  A
-// vector past the row (skip = its width) repeats the last one and stores
-// nothing.
-template <class T, int V, bool TAIL>
-struct Columns {
-  uint32_t col[V], skip[V];
-  __device__ Columns(uint32_t lane, uint32_t tpr, uint32_t dim) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const uint32_t c = (lane + v * tpr) * (uint32_t)kVec<T>;
-      col[v] = c + kVec<T> <= dim ? c : dim - kVec<T>;
-      skip[v] = c >= dim ? kVec<T> : c - col[v];
-    }
-  }
-  __device__ bool any(int v) const { return skip[v] < kVec<T>; }
-  // of a vector with any(v)
-  __device__ bool owns(int v, int e) const { return !TAIL || (uint32_t)e >= skip[v]; }
-};
 
 // A thread's share of the fp32 weight vectors, 1 where the vector is null.  A
 // wave's rows keep it in registers; a block's rows (MULTI) in LDS, [value / 4]
@@ -581,13 +468,6 @@ __global__ __launch_bounds__(kSumCols* kSumGroups) void k_gated_norm_column_sums
 
 int backward_waves(const Shape& s) {
   return s.multi ? kBackwardBlockRowWaves : kBackwardWaves;
-}
-
-unsigned grid_of(int64_t rows, const Shape& s, int waves_per_cu) {
-  const int64_t g = (rows + s.rows_per_block() - 1) / s.rows_per_block();
-  const int per_cu = waves_per_cu / s.waves() > 1 ? waves_per_cu / s.waves() : 1;
-  const int64_t most = (int64_t)kCus * per_cu;
-  return (unsigned)(g < most ? g : most);
 }
 
 // Launch of KERNEL on a shape; a block's rows keep their weights in dynamic
