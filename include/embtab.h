@@ -707,6 +707,51 @@ emb_status_t emb_gated_norm_backward(const void* y, const void* block, const voi
                                      void* dblock, void* dgate, float* dw_post, float* dscale,
                                      float* dw_pre, void* ws, size_t ws_bytes, void* stream);
 
+/* The residual's addition, the norm of the sum and its 8-bit rows for an
+ * exchange, in one pass.  Per row of `dim` values (8 <= dim <= 8192), fp32:
+ *   y = x + block
+ *   h = y * rsqrt(mean(y^2) + eps) * w                  (from the unrounded y)
+ *   amax = max |h|;  code = round-to-nearest-even(h * (127 / amax)),
+ *   scale = amax / 127;  amax == 0: codes and scale 0
+ * the scheme of emb_quantize_rows_int8.  x, block, y: [rows, dim] of `dtype`;
+ * w: fp32 [dim]; codes: int8 [rows, dim], any alignment; scales: fp32 [rows].
+ * A row that holds a value that is not finite, or whose sum of squares is not,
+ * has codes 0 and a NaN for its scale.  y may be x or block; other outputs must
+ * not overlap inputs or each other.  eps >= 0.  The gradients, with the rounding
+ * to 8 bits passed over, are those of emb_gated_norm_backward from y, without a
+ * gate and w_post and with scale 1. */
+emb_status_t emb_add_norm_int8(const void* x, const void* block, const float* w, int64_t rows,
+                               int32_t dim, int32_t dtype, float eps, void* y, int8_t* codes,
+                               float* scales, void* stream);
+
+/* emb_expert_dispatch of 8-bit rows, as the values they stand for:
+ *   xs[r] = codes[src[r] / topk] * scales[src[r] / topk]   (fp32, rounded once),
+ *           0 for an empty row
+ * codes: int8 [tokens, dim], any alignment; scales: fp32 [tokens]; xs: [rows,
+ * dim] of `dtype`.  With topk 1 and pos = src = 0, 1, 2, ... the rows are read
+ * back in their own order.  Its gradient is emb_expert_dispatch_backward's. */
+emb_status_t emb_expert_dispatch_int8(const int8_t* codes, const float* scales,
+                                      const int32_t* pos, const int32_t* src, int64_t tokens,
+                                      int32_t topk, int64_t rows, int32_t dim, int32_t dtype,
+                                      void* xs, void* stream);
+
+/* Dropout whose mask is never stored.  Element i takes 16 bits of a
+ * counter-based random word and is kept where they are below a threshold:
+ *   h = SM(SM(rng[0]) ^ (rng[1] + floor(i / 4)))    (SM = one SplitMix64 step,
+ *   bits = (h >> 16 (i mod 4)) & 0xFFFF              64-bit words)
+ *   keep = round((1 - p) * 2^16)
+ *   y[i] = residual[i] + (bits < keep ? x[i] * (2^16 / keep) : 0)
+ * so p counts in steps of 2^-16 and the scale is the reciprocal of the share
+ * kept in fact.  residual NULL: 0.  A dropped x counts for nothing, whatever it
+ * holds.  The gradient of x is the same call on dy without a residual and with
+ * the same rng.  rng: device int64 [2], seed and counter, 8-byte aligned; the
+ * call leaves it as it is and uses the words counter .. counter +
+ * ceil(numel / 4) - 1, past which the caller's next call starts.  x, residual,
+ * y: [numel] of `dtype`, 0 <= numel < 2^40; y may be x or residual.
+ * 0 <= p <= 1. */
+emb_status_t emb_dropout(const void* x, const void* residual, int64_t numel, int32_t dtype,
+                         double p, const int64_t* rng, void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

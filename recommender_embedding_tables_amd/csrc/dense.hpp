@@ -1,5 +1,5 @@
-// Element types of the dense operators (gradient clip, expert routing, gated
-// norm), 16-byte accesses at element alignment, and their launchers.
+// Element types of the dense operators (gradient clip, expert routing and
+// feed-forward, norms, dropout), 16-byte accesses at element alignment, and their launchers.
 #pragma once
 
 #include "embtab_internal.hpp"
@@ -154,6 +154,10 @@ hipError_t launch_expert_combine_backward(const void* dy, const void* ys, const 
                                           int64_t tokens, int32_t topk, int64_t rows, int32_t dim,
                                           int32_t dtype, void* dys, float* dweights,
                                           hipStream_t s);
+hipError_t launch_expert_dispatch_int8(const int8_t* codes, const float* scales,
+                                       const int32_t* pos, const int32_t* src, int64_t tokens,
+                                       int32_t topk, int64_t rows, int32_t dim, int32_t dtype,
+                                       void* xs, hipStream_t s);
 
 // gated_norm.hip
 struct GatedNorm {
@@ -171,5 +175,20 @@ hipError_t launch_gated_norm_backward(const GatedNorm& a, int32_t dtype, const v
                                       const void* dh, void* dx, void* dblock, void* dgate,
                                       float* dw_post, float* dscale, float* dw_pre, char* ws,
                                       hipStream_t s);
+
+// rows_int8.hip
+struct AddNorm {
+  const void *x, *block;
+  const float* w;
+  int64_t rows;
+  int32_t dim;
+  float eps;
+};
+hipError_t launch_add_norm_int8(const AddNorm& a, int32_t dtype, void* y, int8_t* codes,
+                                float* scales, hipStream_t s);
+
+// dropout.hip; keep: of 2^16 elements
+hipError_t launch_dropout(const void* x, const void* residual, int64_t numel, int32_t dtype,
+                          uint32_t keep, const int64_t* rng, void* y, hipStream_t s);
 
 }  // namespace embtab

@@ -193,4 +193,43 @@ emb_status_t emb_gated_norm_backward(const void* y, const void* block, const voi
                                                static_cast<hipStream_t>(stream)));
 }
 
+emb_status_t emb_add_norm_int8(const void* x, const void* block, const float* w, int64_t rows,
+                               int32_t dim, int32_t dtype, float eps, void* y, int8_t* codes,
+                               float* scales, void* stream) {
+  if (rows < 0 || rows > kMaxRows || dim < 8 || dim > 8192 || !dtype_ok(dtype) ||
+      !(eps >= 0.0f) || !std::isfinite(eps))
+    return EMB_ERR_INVALID_ARG;
+  const size_t a = dtype_size(dtype);
+  if (!data_ok(x, rows, a) || !data_ok(block, rows, a) || !w || !aligned(w, 4) ||
+      !data_ok(y, rows, a) || !data_ok(codes, rows, 1) || !data_ok(scales, rows, 4))
+    return EMB_ERR_INVALID_ARG;
+  return hip_status(launch_add_norm_int8({x, block, w, rows, dim, eps}, dtype, y, codes, scales,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+emb_status_t emb_expert_dispatch_int8(const int8_t* codes, const float* scales,
+                                      const int32_t* pos, const int32_t* src, int64_t tokens,
+                                      int32_t topk, int64_t rows, int32_t dim, int32_t dtype,
+                                      void* xs, void* stream) {
+  if (!rows_ok(tokens, topk, rows, dim, dtype)) return EMB_ERR_INVALID_ARG;
+  if (!data_ok(codes, tokens, 1) || !data_ok(scales, tokens, 4) || !data_ok(pos, tokens, 4) ||
+      !data_ok(src, rows, 4) || !data_ok(xs, rows, dtype_size(dtype)))
+    return EMB_ERR_INVALID_ARG;
+  return hip_status(launch_expert_dispatch_int8(codes, scales, pos, src, tokens, topk, rows, dim,
+                                                dtype, xs, static_cast<hipStream_t>(stream)));
+}
+
+emb_status_t emb_dropout(const void* x, const void* residual, int64_t numel, int32_t dtype,
+                         double p, const int64_t* rng, void* y, void* stream) {
+  if (numel < 0 || numel >= (1ll << 40) || !dtype_ok(dtype) || !(p >= 0.0 && p <= 1.0))
+    return EMB_ERR_INVALID_ARG;
+  const size_t a = dtype_size(dtype);
+  if (!data_ok(x, numel, a) || !aligned(residual, a) || !rng || !aligned(rng, 8) ||
+      !data_ok(y, numel, a))
+    return EMB_ERR_INVALID_ARG;
+  const uint32_t keep = (uint32_t)std::floor((1.0 - p) * 65536.0 + 0.5);
+  return hip_status(launch_dropout(x, residual, numel, dtype, keep, rng, y,
+                                   static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

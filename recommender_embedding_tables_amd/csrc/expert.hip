@@ -238,11 +238,62 @@ __device__ inline void zero_empty_rows(const int32_t* __restrict__ src, int64_t 
   }
 }
 
+// Where a dispatch finds its tokens' rows: values of the type, or 8-bit codes
+// with a scale per row.  Held is a vector as it was loaded, values() what it
+// stands for.
+template <class T>
+struct ValueRows {
+  const T* x;
+  uint32_t dim;
+  typedef Raw<T> Held;
+  __device__ inline Held load(int64_t tok, uint32_t col) const {
+    return load_raw<T, kVec<T>, true>(x + (size_t)tok * dim + col);
+  }
+  static __device__ inline Raw<T> values(const Held& h) { return h; }
+};
+
+typedef u2 u2_at1 __attribute__((aligned(1)));
+typedef uint32_t u1_at1 __attribute__((aligned(1)));
+
+template <class T>
+struct CodeRows {
+  const int8_t* codes;
+  const float* scales;
+  uint32_t dim;
+  struct Held {
+    uint32_t w[kVec<T> / 4];
+    float scale;
+  };
+  __device__ inline Held load(int64_t tok, uint32_t col) const {
+    const int8_t* p = codes + (size_t)tok * dim + col;
+    Held h;
+    if constexpr (kVec<T> == 8) {
+      const u2 v = __builtin_nontemporal_load(reinterpret_cast<const u2_at1*>(p));
+      h.w[0] = v[0];
+      h.w[1] = v[1];
+    } else {
+      h.w[0] = __builtin_nontemporal_load(reinterpret_cast<const u1_at1*>(p));
+    }
+    h.scale = scales[tok];
+    return h;
+  }
+  // code * scale in fp32, rounded once
+  static __device__ inline Raw<T> values(const Held& h) {
+    float v[kVec<T>];
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e)
+      v[e] = (float)(int8_t)(h.w[e >> 2] >> (8 * (e & 3))) * h.scale;
+    Raw<T> r;
+    r.set_all(v);
+    return r;
+  }
+};
+
 // Block b < token_blocks copies tpb tokens; the later blocks zero the empty
 // rows.
-template <class T>
+template <class T, class Rows>
 __global__ __launch_bounds__(kRowThreads) void k_expert_dispatch(
-    const T* __restrict__ x, const int32_t* __restrict__ pos, const int32_t* __restrict__ src,
+    const Rows in, const int32_t* __restrict__ pos, const int32_t* __restrict__ src,
     int64_t tokens, uint32_t topk, int64_t rows, uint32_t dim, uint32_t nvec, uint32_t tpb,
     uint32_t token_blocks, T* __restrict__ xs) {
   const uint32_t block = block_index();
@@ -254,31 +305,32 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_dispatch(
   const uint32_t nt = tokens - t0 < (int64_t)tpb ? (uint32_t)(tokens - t0) : tpb;
   const uint32_t all = nt * nvec;
   for (uint32_t i0 = threadIdx.x; i0 < all; i0 += kRowThreads * kRowVecs) {
-    Raw<T> r[kRowVecs];
+    typename Rows::Held r[kRowVecs];
     uint32_t tok[kRowVecs], col[kRowVecs];
 #pragma unroll
     for (int u = 0; u < kRowVecs; ++u) {
       const uint32_t i = i0 + u * kRowThreads < all ? i0 + u * kRowThreads : all - 1;
       tok[u] = i / nvec;
       col[u] = vec_column<T>(i - tok[u] * nvec, dim);
-      r[u] = load_raw<T, kVec<T>, true>(x + (size_t)(t0 + tok[u]) * dim + col[u]);
+      r[u] = in.load(t0 + tok[u], col[u]);
     }
 #pragma unroll
     for (int u = 0; u < kRowVecs; ++u) {
       if (i0 + u * kRowThreads >= all) break;
       const int32_t* p = pos + (size_t)(t0 + tok[u]) * topk;
+      const Raw<T> v = Rows::values(r[u]);
       for (uint32_t j = 0; j < topk; ++j)
         if ((uint32_t)p[j] < (uint32_t)rows)
-          store_raw<T, kVec<T>, true>(xs + (size_t)p[j] * dim + col[u], r[u]);
+          store_raw<T, kVec<T>, true>(xs + (size_t)p[j] * dim + col[u], v);
     }
   }
 }
 
 // The same with one wave per token for rows that fill its lanes (kWideVecs):
 // its choices are scalars.
-template <class T>
+template <class T, class Rows>
 __global__ __launch_bounds__(kRowThreads) void k_expert_dispatch_wide(
-    const T* __restrict__ x, const int32_t* __restrict__ pos, const int32_t* __restrict__ src,
+    const Rows in, const int32_t* __restrict__ pos, const int32_t* __restrict__ src,
     int64_t tokens, uint32_t topk, int64_t rows, uint32_t dim, uint32_t nvec,
     uint32_t token_blocks, T* __restrict__ xs) {
   const uint32_t block = block_index();
@@ -292,14 +344,17 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_dispatch_wide(
   if (tok >= tokens) return;
   const int32_t* p = pos + (size_t)tok * topk;
   for (uint32_t v0 = 0; v0 < nvec; v0 += 64u * kRowVecs) {
-    Raw<T> r[kRowVecs];
+    typename Rows::Held held[kRowVecs];
     uint32_t col[kRowVecs];
 #pragma unroll
     for (int u = 0; u < kRowVecs; ++u) {
       const uint32_t v = v0 + u * 64u + lane;
       col[u] = vec_column<T>(v < nvec ? v : nvec - 1u, dim);
-      r[u] = load_raw<T, kVec<T>, true>(x + (size_t)tok * dim + col[u]);
+      held[u] = in.load(tok, col[u]);
     }
+    Raw<T> r[kRowVecs];
+#pragma unroll
+    for (int u = 0; u < kRowVecs; ++u) r[u] = Rows::values(held[u]);
     for (uint32_t j = 0; j < topk; ++j) {
       if ((uint32_t)p[j] >= (uint32_t)rows) continue;
       T* row = xs + (size_t)p[j] * dim;
@@ -490,8 +545,8 @@ uint32_t tokens_per_block(uint32_t nvec) {
   return t < 1u ? 1u : t;
 }
 
-template <class T>
-hipError_t dispatch_t(const void* x, const int32_t* pos, const int32_t* src, int64_t tokens,
+template <class T, class Rows>
+hipError_t dispatch_t(const Rows& in, const int32_t* pos, const int32_t* src, int64_t tokens,
                       int32_t topk, int64_t rows, int32_t dim, void* xs, hipStream_t s) {
   const uint32_t nvec = vectors((uint32_t)dim, kVec<T>), tpb = tokens_per_block(nvec);
   const bool wide = nvec >= kWideVecs;
@@ -499,13 +554,13 @@ hipError_t dispatch_t(const void* x, const int32_t* pos, const int32_t* src, int
   const int64_t tb = (tokens + per - 1) / per, zb = (rows + kZeroRows - 1) / kZeroRows;
   if (tb + zb == 0) return hipSuccess;
   if (wide)
-    hipLaunchKernelGGL((k_expert_dispatch_wide<T>), row_grid(tb + zb), dim3(kRowThreads),
-                       0, s, static_cast<const T*>(x), pos, src, tokens, (uint32_t)topk, rows,
-                       (uint32_t)dim, nvec, (uint32_t)tb, static_cast<T*>(xs));
+    hipLaunchKernelGGL((k_expert_dispatch_wide<T, Rows>), row_grid(tb + zb), dim3(kRowThreads),
+                       0, s, in, pos, src, tokens, (uint32_t)topk, rows, (uint32_t)dim, nvec,
+                       (uint32_t)tb, static_cast<T*>(xs));
   else
-    hipLaunchKernelGGL((k_expert_dispatch<T>), row_grid(tb + zb), dim3(kRowThreads), 0, s,
-                       static_cast<const T*>(x), pos, src, tokens, (uint32_t)topk, rows,
-                       (uint32_t)dim, nvec, tpb, (uint32_t)tb, static_cast<T*>(xs));
+    hipLaunchKernelGGL((k_expert_dispatch<T, Rows>), row_grid(tb + zb), dim3(kRowThreads), 0, s,
+                       in, pos, src, tokens, (uint32_t)topk, rows, (uint32_t)dim, nvec, tpb,
+                       (uint32_t)tb, static_cast<T*>(xs));
   return hipGetLastError();
 }
 
@@ -620,13 +675,46 @@ hipError_t launch_expert_sort(const int64_t* ids, int64_t tokens, int32_t topk, 
   return hipGetLastError();
 }
 
+namespace {
+
+template <class T>
+hipError_t dispatch_values(const void* x, const int32_t* pos, const int32_t* src, int64_t tokens,
+                           int32_t topk, int64_t rows, int32_t dim, void* xs, hipStream_t s) {
+  return dispatch_t<T>(ValueRows<T>{static_cast<const T*>(x), (uint32_t)dim}, pos, src, tokens,
+                       topk, rows, dim, xs, s);
+}
+
+template <class T>
+hipError_t dispatch_codes(const int8_t* codes, const float* scales, const int32_t* pos,
+                          const int32_t* src, int64_t tokens, int32_t topk, int64_t rows,
+                          int32_t dim, void* xs, hipStream_t s) {
+  return dispatch_t<T>(CodeRows<T>{codes, scales, (uint32_t)dim}, pos, src, tokens, topk, rows,
+                       dim, xs, s);
+}
+
+}  // namespace
+
 hipError_t launch_expert_dispatch(const void* x, const int32_t* pos, const int32_t* src,
                                   int64_t tokens, int32_t topk, int64_t rows, int32_t dim,
                                   int32_t dtype, void* xs, hipStream_t s) {
   switch (dtype) {
-    case EMB_F32: return dispatch_t<float>(x, pos, src, tokens, topk, rows, dim, xs, s);
-    case EMB_BF16: return dispatch_t<bf16_t>(x, pos, src, tokens, topk, rows, dim, xs, s);
-    default: return dispatch_t<f16_t>(x, pos, src, tokens, topk, rows, dim, xs, s);
+    case EMB_F32: return dispatch_values<float>(x, pos, src, tokens, topk, rows, dim, xs, s);
+    case EMB_BF16: return dispatch_values<bf16_t>(x, pos, src, tokens, topk, rows, dim, xs, s);
+    default: return dispatch_values<f16_t>(x, pos, src, tokens, topk, rows, dim, xs, s);
+  }
+}
+
+hipError_t launch_expert_dispatch_int8(const int8_t* codes, const float* scales,
+                                       const int32_t* pos, const int32_t* src, int64_t tokens,
+                                       int32_t topk, int64_t rows, int32_t dim, int32_t dtype,
+                                       void* xs, hipStream_t s) {
+  switch (dtype) {
+    case EMB_F32:
+      return dispatch_codes<float>(codes, scales, pos, src, tokens, topk, rows, dim, xs, s);
+    case EMB_BF16:
+      return dispatch_codes<bf16_t>(codes, scales, pos, src, tokens, topk, rows, dim, xs, s);
+    default:
+      return dispatch_codes<f16_t>(codes, scales, pos, src, tokens, topk, rows, dim, xs, s);
   }
 }
 

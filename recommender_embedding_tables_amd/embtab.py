@@ -65,6 +65,7 @@ EXPORTED = [
     "emb_expert_workspace_bytes", "emb_expert_sort", "emb_expert_dispatch", "emb_expert_combine",
     "emb_expert_combine_backward", "emb_expert_dispatch_backward",
     "emb_gated_norm_workspace_bytes", "emb_gated_norm_forward", "emb_gated_norm_backward",
+    "emb_add_norm_int8", "emb_expert_dispatch_int8", "emb_dropout",
 ]
 
 EMB_PHASE_FORWARD, EMB_PHASE_KEYS, EMB_PHASE_SORT, EMB_PHASE_UNIQUE = 0, 1, 2, 3
@@ -188,6 +189,9 @@ def _load():
         "emb_gated_norm_forward": (i32, [P, P, P, P, P, P, i64, i32, i32, i32, f32, P, P, P]),
         "emb_gated_norm_backward": (i32, [P, P, P, P, P, P, P, P, i64, i32, i32, i32, f32, P, P,
                                           P, P, P, P, P, sz, P]),
+        "emb_add_norm_int8": (i32, [P, P, P, i64, i32, i32, f32, P, P, P, P]),
+        "emb_expert_dispatch_int8": (i32, [P, P, P, P, i64, i32, i64, i32, i32, P, P]),
+        "emb_dropout": (i32, [P, P, i64, i32, C.c_double, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -664,3 +668,19 @@ def emb_gated_norm_backward(y, block, gate, w_post, scale, w_pre, dy, dh, rows, 
                                         dtype, gate_kind, eps, _ptr(dx), _ptr(dblock),
                                         _ptr(dgate), _ptr(dw_post), _ptr(dscale), _ptr(dw_pre),
                                         _ptr(ws), ws_bytes, _stream(stream))
+
+
+def emb_add_norm_int8(x, block, w, rows, dim, dtype, eps, y, codes, scales, stream=None) -> int:
+    return _lib.emb_add_norm_int8(_ptr(x), _ptr(block), _ptr(w), rows, dim, dtype, eps, _ptr(y),
+                                  _ptr(codes), _ptr(scales), _stream(stream))
+
+
+def emb_expert_dispatch_int8(codes, scales, pos, src, tokens, topk, rows, dim, dtype, xs,
+                             stream=None) -> int:
+    return _lib.emb_expert_dispatch_int8(_ptr(codes), _ptr(scales), _ptr(pos), _ptr(src), tokens,
+                                         topk, rows, dim, dtype, _ptr(xs), _stream(stream))
+
+
+def emb_dropout(x, residual, numel, dtype, p, rng, y, stream=None) -> int:
+    return _lib.emb_dropout(_ptr(x), _ptr(residual), numel, dtype, p, _ptr(rng), _ptr(y),
+                            _stream(stream))
