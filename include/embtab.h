@@ -707,6 +707,54 @@ emb_status_t emb_gated_norm_backward(const void* y, const void* block, const voi
                                      void* dblock, void* dgate, float* dw_post, float* dscale,
                                      float* dw_pre, void* ws, size_t ws_bytes, void* stream);
 
+/* The experts' gated feed-forward, on rows in expert order (emb_expert_dispatch)
+ * or, dense, on all rows with one expert.  Per row x of expert e:
+ *   g = Wg x;  u = Wu x        (w_in[e] = Wg over Wu)
+ *   a = act(g) * u
+ *   y = Wo a                   (w_out[e] = Wo)
+ *   x, y   [rows, dim]          w_in   [experts, 2 * hidden, dim]
+ *   gu     [rows, 2 * hidden]   w_out  [experts, dim, hidden]
+ *   a      [rows, hidden]       all of `dtype`
+ *   offsets int32 [experts + 1] as emb_expert_sort writes them; NULL with one
+ *          expert: every row is its
+ *   rows, capacity  the buffer's M rows and the capacity of emb_expert_sort
+ *          (rows = experts * capacity, or capacity 0)
+ * The rows of no expert are neither read nor written.  The sums are in fp32;
+ * gu, a and y are rounded once each, and y is formed from the rounded a.  gu
+ * and a are what the backward needs: gu NULL where it is not wanted.  An
+ * infinite fp32 input gives NaN or an infinity.
+ *
+ * The backward takes gu and a as the forward stored them:
+ *   da = Wo' dy;  du = da * act(g);  dg = da * u * act'(g)   (rounded to dtype)
+ *   dx = Wg' dg + Wu' du
+ *   dw_in[e] = sum over the expert's rows of (dg over du) x';  dw_out[e] = sum of
+ *   dy a'; zeros for an expert without rows
+ * each sum in fp32 and rounded once.  dw_in, dw_out: as the weights.
+ *
+ * 8 <= dim, hidden <= 65536; 1 <= experts <= 1024; rows * dim and rows * hidden
+ * below 2^40.  Outputs must not overlap inputs or each other.  Offsets that are
+ * not ascending inside [0, rows] give results without meaning, but no access
+ * outside the buffers. */
+typedef enum {
+  EMB_ACT_SILU = 0,    /* v / (1 + e^-v) */
+  EMB_ACT_GELU = 1,    /* v (1 + erf(v / sqrt 2)) / 2 */
+  EMB_ACT_RELU = 2,    /* max(v, 0) */
+  EMB_ACT_SIGMOID = 3  /* 1 / (1 + e^-v) */
+} emb_act_t;
+size_t emb_gated_ffn_workspace_bytes(int64_t rows, int32_t experts, int32_t dim, int32_t hidden,
+                                     int32_t dtype);
+emb_status_t emb_gated_ffn_forward(const void* x, const void* w_in, const void* w_out,
+                                   const int32_t* offsets, int64_t rows, int32_t experts,
+                                   int64_t capacity, int32_t dim, int32_t hidden, int32_t dtype,
+                                   int32_t act, void* gu, void* a, void* y, void* ws,
+                                   size_t ws_bytes, void* stream);
+emb_status_t emb_gated_ffn_backward(const void* x, const void* gu, const void* a,
+                                    const void* w_in, const void* w_out, const void* dy,
+                                    const int32_t* offsets, int64_t rows, int32_t experts,
+                                    int64_t capacity, int32_t dim, int32_t hidden, int32_t dtype,
+                                    int32_t act, void* dx, void* dw_in, void* dw_out, void* ws,
+                                    size_t ws_bytes, void* stream);
+
 /* The residual's addition, the norm of the sum and its 8-bit rows for an
  * exchange, in one pass.  Per row of `dim` values (8 <= dim <= 8192), fp32:
  *   y = x + block

@@ -176,6 +176,21 @@ hipError_t launch_gated_norm_backward(const GatedNorm& a, int32_t dtype, const v
                                       float* dw_post, float* dscale, float* dw_pre, char* ws,
                                       hipStream_t s);
 
+// ffn_f32.hip, ffn_bf16.hip, ffn_f16.hip
+struct GatedFfn {
+  const void *x, *w_in, *w_out;
+  const int32_t* offsets;
+  int64_t rows, capacity;
+  int32_t experts, dim, hidden, act;
+};
+template <class T>
+size_t ffn_workspace_bytes_t(int64_t rows, int32_t experts, int64_t dim, int64_t hidden);
+template <class T>
+hipError_t ffn_forward_t(const GatedFfn& f, void* gu, void* a, void* y, char* ws, hipStream_t s);
+template <class T>
+hipError_t ffn_backward_t(const GatedFfn& f, const void* gu, const void* a, const void* dy,
+                          void* dx, void* dw_in, void* dw_out, char* ws, hipStream_t s);
+
 // rows_int8.hip
 struct AddNorm {
   const void *x, *block;

@@ -56,6 +56,34 @@ bool gated_norm_ok(const GatedNorm& a, int32_t dtype, int32_t gate_kind) {
          a.scale && aligned(a.scale, 4) && a.w_pre && aligned(a.w_pre, 4);
 }
 
+// Sizes of the feed-forward.  rows * dim and rows * hidden stay below 2^40, so
+// every launch has fewer than 2^31 blocks.
+bool ffn_shape_ok(int64_t rows, int32_t experts, int32_t dim, int32_t hidden, int32_t dtype) {
+  return rows >= 0 && rows <= kMaxRows && experts >= 1 && experts <= 1024 && dim >= 8 &&
+         dim <= 65536 && hidden >= 8 && hidden <= 65536 && dtype_ok(dtype) &&
+         rows * dim < (1ll << 40) && rows * hidden < (1ll << 40);
+}
+
+bool ffn_ok(const GatedFfn& f, int32_t dtype) {
+  if (!ffn_shape_ok(f.rows, f.experts, f.dim, f.hidden, dtype)) return false;
+  if (f.act < EMB_ACT_SILU || f.act > EMB_ACT_SIGMOID) return false;
+  if (f.offsets ? !aligned(f.offsets, 4) : f.experts != 1 || f.capacity != 0) return false;
+  if (f.capacity < 0 || f.capacity > kMaxRows ||
+      (f.capacity > 0 && f.rows != f.capacity * f.experts))
+    return false;
+  const size_t a = dtype_size(dtype);
+  return data_ok(f.x, f.rows, a) && f.w_in && aligned(f.w_in, a) && f.w_out &&
+         aligned(f.w_out, a);
+}
+
+size_t ffn_workspace(int64_t rows, int32_t experts, int32_t dim, int32_t hidden, int32_t dtype) {
+  switch (dtype) {
+    case EMB_F32: return ffn_workspace_bytes_t<float>(rows, experts, dim, hidden);
+    case EMB_BF16: return ffn_workspace_bytes_t<bf16_t>(rows, experts, dim, hidden);
+    default: return ffn_workspace_bytes_t<f16_t>(rows, experts, dim, hidden);
+  }
+}
+
 }  // namespace
 
 extern "C" {
@@ -191,6 +219,57 @@ emb_status_t emb_gated_norm_backward(const void* y, const void* block, const voi
   return hip_status(launch_gated_norm_backward(a, dtype, dy, dh, dx, dblock, dgate, dw_post,
                                                dscale, dw_pre, static_cast<char*>(ws),
                                                static_cast<hipStream_t>(stream)));
+}
+
+size_t emb_gated_ffn_workspace_bytes(int64_t rows, int32_t experts, int32_t dim, int32_t hidden,
+                                     int32_t dtype) {
+  if (!ffn_shape_ok(rows, experts, dim, hidden, dtype)) return 0;
+  return ffn_workspace(rows, experts, dim, hidden, dtype);
+}
+
+emb_status_t emb_gated_ffn_forward(const void* x, const void* w_in, const void* w_out,
+                                   const int32_t* offsets, int64_t rows, int32_t experts,
+                                   int64_t capacity, int32_t dim, int32_t hidden, int32_t dtype,
+                                   int32_t act, void* gu, void* a, void* y, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  const GatedFfn f{x, w_in, w_out, offsets, rows, capacity, experts, dim, hidden, act};
+  if (!ffn_ok(f, dtype)) return EMB_ERR_INVALID_ARG;
+  const size_t al = dtype_size(dtype);
+  if (!aligned(gu, al) || !data_ok(a, rows, al) || !data_ok(y, rows, al))
+    return EMB_ERR_INVALID_ARG;
+  if (!workspace_ok(ws, ws_bytes, ffn_workspace(rows, experts, dim, hidden, dtype)))
+    return EMB_ERR_WORKSPACE;
+  char* w = static_cast<char*>(ws);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (dtype) {
+    case EMB_F32: return hip_status(ffn_forward_t<float>(f, gu, a, y, w, s));
+    case EMB_BF16: return hip_status(ffn_forward_t<bf16_t>(f, gu, a, y, w, s));
+    default: return hip_status(ffn_forward_t<f16_t>(f, gu, a, y, w, s));
+  }
+}
+
+emb_status_t emb_gated_ffn_backward(const void* x, const void* gu, const void* a,
+                                    const void* w_in, const void* w_out, const void* dy,
+                                    const int32_t* offsets, int64_t rows, int32_t experts,
+                                    int64_t capacity, int32_t dim, int32_t hidden, int32_t dtype,
+                                    int32_t act, void* dx, void* dw_in, void* dw_out, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  const GatedFfn f{x, w_in, w_out, offsets, rows, capacity, experts, dim, hidden, act};
+  if (!ffn_ok(f, dtype)) return EMB_ERR_INVALID_ARG;
+  const size_t al = dtype_size(dtype);
+  if (!data_ok(gu, rows, al) || !data_ok(a, rows, al) || !data_ok(dy, rows, al) ||
+      !data_ok(dx, rows, al) || !dw_in || !aligned(dw_in, al) || !dw_out || !aligned(dw_out, al))
+    return EMB_ERR_INVALID_ARG;
+  if (!workspace_ok(ws, ws_bytes, ffn_workspace(rows, experts, dim, hidden, dtype)))
+    return EMB_ERR_WORKSPACE;
+  char* w = static_cast<char*>(ws);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (dtype) {
+    case EMB_F32: return hip_status(ffn_backward_t<float>(f, gu, a, dy, dx, dw_in, dw_out, w, s));
+    case EMB_BF16:
+      return hip_status(ffn_backward_t<bf16_t>(f, gu, a, dy, dx, dw_in, dw_out, w, s));
+    default: return hip_status(ffn_backward_t<f16_t>(f, gu, a, dy, dx, dw_in, dw_out, w, s));
+  }
 }
 
 emb_status_t emb_add_norm_int8(const void* x, const void* block, const float* w, int64_t rows,

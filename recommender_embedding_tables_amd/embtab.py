@@ -44,6 +44,8 @@ EMB_F32, EMB_BF16, EMB_F16 = 0, 1, 2
 
 EMB_GATE_NONE, EMB_GATE_ROW, EMB_GATE_ELEMENT, EMB_GATE_SIGMOID = 0, 1, 2, 4
 
+EMB_ACT_SILU, EMB_ACT_GELU, EMB_ACT_RELU, EMB_ACT_SIGMOID = 0, 1, 2, 3
+
 EMB_EMPTY_KEY = 0xFFFFFFFFFFFFFFFF
 
 EXPORTED = [
@@ -65,6 +67,7 @@ EXPORTED = [
     "emb_expert_workspace_bytes", "emb_expert_sort", "emb_expert_dispatch", "emb_expert_combine",
     "emb_expert_combine_backward", "emb_expert_dispatch_backward",
     "emb_gated_norm_workspace_bytes", "emb_gated_norm_forward", "emb_gated_norm_backward",
+    "emb_gated_ffn_workspace_bytes", "emb_gated_ffn_forward", "emb_gated_ffn_backward",
     "emb_add_norm_int8", "emb_expert_dispatch_int8", "emb_dropout",
 ]
 
@@ -189,6 +192,11 @@ def _load():
         "emb_gated_norm_forward": (i32, [P, P, P, P, P, P, i64, i32, i32, i32, f32, P, P, P]),
         "emb_gated_norm_backward": (i32, [P, P, P, P, P, P, P, P, i64, i32, i32, i32, f32, P, P,
                                           P, P, P, P, P, sz, P]),
+        "emb_gated_ffn_workspace_bytes": (sz, [i64, i32, i32, i32, i32]),
+        "emb_gated_ffn_forward": (i32, [P, P, P, P, i64, i32, i64, i32, i32, i32, i32, P, P, P,
+                                        P, sz, P]),
+        "emb_gated_ffn_backward": (i32, [P, P, P, P, P, P, P, i64, i32, i64, i32, i32, i32, i32,
+                                         P, P, P, P, sz, P]),
         "emb_add_norm_int8": (i32, [P, P, P, i64, i32, i32, f32, P, P, P, P]),
         "emb_expert_dispatch_int8": (i32, [P, P, P, P, i64, i32, i64, i32, i32, P, P]),
         "emb_dropout": (i32, [P, P, i64, i32, C.c_double, P, P, P]),
@@ -668,6 +676,26 @@ def emb_gated_norm_backward(y, block, gate, w_post, scale, w_pre, dy, dh, rows, 
                                         dtype, gate_kind, eps, _ptr(dx), _ptr(dblock),
                                         _ptr(dgate), _ptr(dw_post), _ptr(dscale), _ptr(dw_pre),
                                         _ptr(ws), ws_bytes, _stream(stream))
+
+
+def emb_gated_ffn_workspace_bytes(rows, experts, dim, hidden, dtype) -> int:
+    return int(_lib.emb_gated_ffn_workspace_bytes(rows, experts, dim, hidden, dtype))
+
+
+def emb_gated_ffn_forward(x, w_in, w_out, offsets, rows, experts, capacity, dim, hidden, dtype,
+                          act, gu, a, y, ws, ws_bytes, stream=None) -> int:
+    return _lib.emb_gated_ffn_forward(_ptr(x), _ptr(w_in), _ptr(w_out), _ptr(offsets), rows,
+                                      experts, capacity, dim, hidden, dtype, act, _ptr(gu),
+                                      _ptr(a), _ptr(y), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def emb_gated_ffn_backward(x, gu, a, w_in, w_out, dy, offsets, rows, experts, capacity, dim,
+                           hidden, dtype, act, dx, dw_in, dw_out, ws, ws_bytes,
+                           stream=None) -> int:
+    return _lib.emb_gated_ffn_backward(_ptr(x), _ptr(gu), _ptr(a), _ptr(w_in), _ptr(w_out),
+                                       _ptr(dy), _ptr(offsets), rows, experts, capacity, dim,
+                                       hidden, dtype, act, _ptr(dx), _ptr(dw_in), _ptr(dw_out),
+                                       _ptr(ws), ws_bytes, _stream(stream))
 
 
 def emb_add_norm_int8(x, block, w, rows, dim, dtype, eps, y, codes, scales, stream=None) -> int:
