@@ -47,18 +47,28 @@ inline int64_t row_tiles_bound(const Groups& g, int64_t tile) {
 }
 
 // ---------------------------------------------------------------- tile order
-// Blocks go to the 8 XCDs in turn, each with an L2 of its own: block b takes
-// place (b mod 8) * per + b / 8 of the order, so that an XCD works on
-// neighbouring tiles.  Inside a group, panels of kPanel row tiles walk over the
-// column tiles with the rows innermost: 32 blocks of an XCD share 8 row and 4
-// column tiles.
+// Blocks go to the 8 XCDs in turn, each with an L2 of its own.  The order is cut
+// into chunks which the XCDs take in turn: an XCD works on neighbouring tiles, and
+// the tiles of a long group are spread over all of them.  Inside a group, panels
+// of kPanel row tiles walk over the column tiles with the rows innermost.  Chunks
+// of 32 tiles (8 row and 4 column tiles), one for each CU of an XCD, where every
+// tile costs the same; weight gradients, whose tiles cost their expert's rows,
+// take chunks of 8.
 constexpr uint32_t kXcds = 8, kPanel = 8;
+constexpr uint32_t kRowChunk = 32, kWeightChunk = 8;
 
-__device__ inline bool place_of(uint32_t block, uint64_t all, uint64_t& place) {
-  const uint64_t per = (all + kXcds - 1) / kXcds;
-  const uint64_t i = block / kXcds;
-  place = (block % kXcds) * per + i;
-  return i < per && place < all;
+__device__ inline bool place_of(uint32_t block, uint64_t all, uint32_t longest, uint64_t& place) {
+  const uint64_t even = (all + kXcds - 1) / kXcds;
+  const uint32_t chunk = even < longest ? (uint32_t)even : longest;
+  if (chunk == 0) return false;
+  const uint32_t i = block / kXcds;
+  place = ((uint64_t)(i / chunk) * kXcds + block % kXcds) * chunk + i % chunk;
+  return place < all;
+}
+// Blocks that hold the places of up to `most` tiles.
+inline int64_t blocks_of(int64_t most, int64_t longest) {
+  const int64_t whole = kXcds * (most > kXcds * longest ? longest : 1);
+  return (most + whole - 1) / whole * whole;
 }
 
 __device__ inline void panel_tile(uint32_t local, uint32_t row_tiles, uint32_t col_tiles,
@@ -83,7 +93,7 @@ __device__ inline bool find_row_tile(const Groups& g, uint32_t tile, uint32_t co
   if (!g.offsets) {
     const uint32_t n = (uint32_t)((g.rows + tile - 1) / tile);
     uint64_t place;
-    if (!place_of(block, (uint64_t)n * col_tiles, place)) return false;
+    if (!place_of(block, (uint64_t)n * col_tiles, kRowChunk, place)) return false;
     t.expert = 0;
     t.first = 0;
     t.count = g.rows;
@@ -99,7 +109,7 @@ __device__ inline bool find_row_tile(const Groups& g, uint32_t tile, uint32_t co
     total += (uint32_t)__builtin_amdgcn_readlane((int)wave_incl_scan(n), 63);
   }
   uint64_t place;
-  if (!place_of(block, (uint64_t)total * col_tiles, place)) return false;
+  if (!place_of(block, (uint64_t)total * col_tiles, kRowChunk, place)) return false;
   const uint32_t want = (uint32_t)(place / col_tiles);  // in row tiles of the groups in order
   uint32_t before = 0;
   for (int32_t e0 = 0; e0 < g.experts; e0 += 64) {
@@ -122,6 +132,62 @@ __device__ inline bool find_row_tile(const Groups& g, uint32_t tile, uint32_t co
     before = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
   }
   return false;
+}
+
+// Two products of the experts' rows in one launch, C[p][m, n] = sum over one
+// expert's rows of A[p][row, m] B[p][row, n], and the tile of them that a block
+// computes.  Experts go in the order of their rows, the longest first (up to 64
+// experts; more even out by themselves), so that no long one is left to the end.
+template <class T>
+struct WeightProducts {
+  Groups groups;
+  const T *A[2], *B[2];
+  int64_t M[2], N[2];
+  uint32_t row_tiles[2], col_tiles[2];
+  uint32_t parts;  // that an expert's rows are cut into
+};
+struct WeightTile {
+  int32_t expert, product;
+  uint32_t part, rt, ct;
+};
+
+__device__ inline int32_t expert_by_rows(const Groups& g, int32_t place) {
+  if (g.experts > 64) return place;
+  const int lane = threadIdx.x & 63;
+  const int32_t n = lane < g.experts ? (int32_t)group_of(g, lane).count : -1;
+  int32_t before = 0;
+  for (int32_t e = 0; e < g.experts; ++e) {
+    const int32_t other = __builtin_amdgcn_readlane(n, e);
+    before += other > n || (other == n && e < lane);
+  }
+  return (int32_t)__builtin_ctzll(__ballot(lane < g.experts && before == place));
+}
+
+template <class T>
+__device__ inline bool find_weight_tile(const WeightProducts<T>& w, uint32_t block,
+                                        WeightTile& t) {
+  const uint32_t first = w.row_tiles[0] * w.col_tiles[0];
+  const uint32_t tiles = first + w.row_tiles[1] * w.col_tiles[1];
+  uint64_t place;
+  if (!place_of(block, (uint64_t)tiles * w.parts * w.groups.experts, kWeightChunk, place))
+    return false;
+  const uint32_t matrix = (uint32_t)(place / tiles);
+  uint32_t local = (uint32_t)(place - (uint64_t)matrix * tiles);
+  t.expert = expert_by_rows(w.groups, (int32_t)(matrix / w.parts));
+  t.part = matrix % w.parts;
+  t.product = local >= first;
+  if (t.product) local -= first;
+  panel_tile(local, w.row_tiles[t.product], w.col_tiles[t.product], t.rt, t.ct);
+  return true;
+}
+
+// Rows `from` .. `from + count` of expert e's group that part `part` adds up, in
+// whole steps.
+__device__ inline void part_rows(const Group& g, uint32_t parts, uint32_t part, int64_t step,
+                                 int64_t& from, int64_t& count) {
+  const int64_t per = ((g.count + parts - 1) / parts + step - 1) / step * step;
+  from = per * part < g.count ? per * part : g.count;
+  count = g.count - from < per ? g.count - from : per;
 }
 
 inline dim3 tile_grid(int64_t blocks, int threads) {
@@ -190,47 +256,42 @@ __device__ inline void store4(T* p, f32x4 v, int64_t n) {
     if (i < n) p[i] = from_f32<T>(v[i]);
 }
 
+// The first n of four neighbouring values, then zeros.
 template <class T>
-__device__ inline f32x4 load4(const T* p, int64_t n) {
-  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (n >= 4) {
-    if constexpr (sizeof(T) == 4) {
-      const Raw<float> r = load_raw(p);
+__device__ inline Raw<T, 4> load_part4(const T* p, int64_t n) {
+  if (n >= 4) return load_raw<T, 4>(p);
+  float f[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = r.get(i);
-    } else {
-      const Raw<T, 4> r = load_raw<T, 4>(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = r.get(i);
-    }
-    return v;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < n) v[i] = to_f32(p[i]);
-  return v;
+  for (int i = 0; i < 4; ++i) f[i] = i < n ? to_f32(p[i]) : 0.0f;
+  Raw<T, 4> r;
+  r.set_all(f);
+  return r;
 }
 
 // ---------------------------------------------------------------- epilogues
-// Of four neighbouring columns from n on, of `width`, in row `row` (of the
-// buffer; of the expert's matrix for weight gradients).
+// Of four neighbouring columns from n on, of `width`, in row `row` of the buffer.  held(): what it reads of
+// them, for callers that have these loads on their way before they are needed.
+struct NothingHeld {};
+
 template <class T>
 struct StoreEpilogue {
   static constexpr bool kDual = false;
   T* out;
-  int64_t width, expert_stride;
-  __device__ inline void operator()(int32_t e, int64_t row, int64_t n, f32x4 v) const {
-    store4(out + e * expert_stride + row * width + n, v, width - n);
+  int64_t width;
+  typedef NothingHeld Held;
+  __device__ inline Held held(int64_t, int64_t) const { return {}; }
+  __device__ inline void operator()(int64_t row, int64_t n, f32x4 v, Held) const {
+    store4(out + row * width + n, v, width - n);
   }
 };
 
-// Partial sums of weight gradients, one matrix per part.
-struct PartEpilogue {
-  static constexpr bool kDual = false;
-  float* out;
-  int64_t width, expert_stride;
-  __device__ inline void operator()(int32_t e, int64_t row, int64_t n, f32x4 v) const {
-    store4(out + e * expert_stride + row * width + n, v, width - n);
+// Weight gradients: the expert's matrices, or the parts' sums, [expert][part].
+template <class Out>
+struct WeightEpilogue {
+  Out* out[2];
+  __device__ inline void operator()(int32_t product, int64_t matrix, int64_t M, int64_t N,
+                                    int64_t m, int64_t n, f32x4 v) const {
+    store4(out[product] + (matrix * M + m) * N + n, v, N - n);
   }
 };
 
@@ -241,7 +302,10 @@ struct ActEpilogue {
   T *gu, *a;  // gu: null where it is not kept
   int64_t width;
   int32_t act;
-  __device__ inline void operator()(int32_t, int64_t row, int64_t n, f32x4 g, f32x4 u) const {
+  typedef NothingHeld Held;
+  __device__ inline Held held(int64_t, int64_t) const { return {}; }
+  __device__ inline void operator()(int64_t row, int64_t n, f32x4 g, f32x4 u,
+                                    Held) const {
     const int64_t have = width - n;
     if (gu) {
       store4(gu + row * 2 * width + n, g, have);
@@ -262,11 +326,22 @@ struct ActGradEpilogue {
   T* dgu;
   int64_t width;
   int32_t act;
-  __device__ inline void operator()(int32_t, int64_t row, int64_t n, f32x4 da) const {
+  struct Held {
+    Raw<T, 4> g, u;
+  };
+  __device__ inline Held held(int64_t row, int64_t n) const {
+    return {load_part4(gu + row * 2 * width + n, width - n),
+            load_part4(gu + (row * 2 + 1) * width + n, width - n)};
+  }
+  __device__ inline void operator()(int64_t row, int64_t n, f32x4 da,
+                                    const Held& h) const {
     const int64_t have = width - n;
-    const f32x4 g = load4(gu + row * 2 * width + n, have);
-    const f32x4 u = load4(gu + (row * 2 + 1) * width + n, have);
-    f32x4 dg, du;
+    f32x4 g, u, dg, du;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      g[i] = h.g.get(i);
+      u[i] = h.u.get(i);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const ActValue f = act_value<T>(act, g[i]);

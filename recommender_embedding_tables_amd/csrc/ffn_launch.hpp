@@ -2,23 +2,26 @@
 // one source per type).
 #pragma once
 
-#include "ffn_tiles.hpp"
+#include "ffn_wide.hpp"
 
 namespace embtab {
 
 namespace {
 
-// Weight gradients with fewer tiles than this cut the rows into parts, whose
-// sums a second kernel adds in order.
+// Weight gradients with fewer blocks than this cut the experts' rows into parts,
+// whose sums a second kernel adds in order.
 constexpr int64_t kWeightBlocks = 512;
 constexpr int64_t kMaxParts = 16, kPartRows = 256;
 
-int64_t weight_tiles(int64_t m, int64_t n) {
-  return ((m + kTileO - 1) / kTileO) * ((n + kTileO - 1) / kTileO);
+int64_t tiles_of(int64_t m, int64_t n, int64_t tile) {
+  return ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
 }
 
-int64_t weight_parts(int64_t rows, int32_t experts, int64_t m, int64_t n) {
-  const int64_t blocks = weight_tiles(m, n) * experts;
+// dw_in and dw_out of every expert; 128 x 128 tiles count for the rule in both
+// kernels (the workspace does not depend on alignment).
+int64_t weight_parts(int64_t rows, int32_t experts, int64_t dim, int64_t hidden) {
+  const int64_t blocks =
+      (tiles_of(2 * hidden, dim, kTileO) + tiles_of(dim, hidden, kTileO)) * experts;
   int64_t parts = kWeightBlocks / blocks;
   const int64_t most = rows / experts / kPartRows;
   parts = parts < most ? parts : most;
@@ -32,9 +35,9 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t dgu_bytes(int64_t rows, int64_t hidden, size_t size) {
   return align256((size_t)rows * 2 * hidden * size);
 }
-size_t parts_bytes(int64_t rows, int32_t experts, int64_t m, int64_t n) {
-  const int64_t p = weight_parts(rows, experts, m, n);
-  return p > 1 ? align256((size_t)p * experts * m * n * 4) : 0;
+size_t parts_bytes(int64_t rows, int32_t experts, int64_t dim, int64_t hidden) {
+  const int64_t p = weight_parts(rows, experts, dim, hidden);
+  return p > 1 ? align256((size_t)p * experts * 3 * hidden * dim * 4) : 0;
 }
 
 // out[e] = the sum of the expert's parts, in order.
@@ -47,20 +50,38 @@ __global__ __launch_bounds__(256) void k_ffn_add_parts(const float* __restrict__
   const int64_t e = v / per, i = (v - e * per) * 4;
   if (e >= experts) return;
   const float* p = sums + e * parts * size + i;
-  f32x4 t = load4(p, size - i);
-  for (uint32_t k = 1; k < parts; ++k) t += load4(p + k * size, size - i);
+  f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (uint32_t k = 0; k < parts; ++k) {
+    const Raw<float> v4 = load_part4(p + k * size, size - i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] += v4.get(j);
+  }
   store4(out + e * size + i, t, size - i);
 }
 
-int64_t blocks_of(int64_t tiles) { return (tiles + kXcds - 1) / kXcds * kXcds; }
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // C = A B' or A B (B_KC) over the groups' rows
 template <class T, bool B_KC, class Epilogue>
 hipError_t rows_product(const Groups& g, const void* a, const void* b, int64_t K, int64_t N,
                         int64_t b_stride, const Epilogue& epilogue, hipStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (K % 8 == 0 && (B_KC || N % 8 == 0) && on16(a) && on16(b)) {
+      constexpr int WM = 2, WN = 4;
+      const int64_t cols = Epilogue::kDual ? kWideO / 2 : kWideO;
+      const int64_t col_tiles = (N + cols - 1) / cols;
+      const int64_t blocks = blocks_of(row_tiles_bound(g, kWideO) * col_tiles, kRowChunk);
+      if (blocks == 0) return hipSuccess;
+      hipLaunchKernelGGL((k_ffn_rows_wide<T, B_KC, Epilogue, WM, WN>),
+                         tile_grid(blocks, 64 * WM * WN), dim3(64 * WM * WN), 0, s, g,
+                         static_cast<const T*>(a), static_cast<const T*>(b), K, N, b_stride,
+                         (uint32_t)col_tiles, epilogue);
+      return hipGetLastError();
+    }
+  }
   const int64_t cols = Epilogue::kDual ? kTileO / 2 : kTileO;
   const int64_t col_tiles = (N + cols - 1) / cols;
-  const int64_t blocks = blocks_of(row_tiles_bound(g, kTileO) * col_tiles);
+  const int64_t blocks = blocks_of(row_tiles_bound(g, kTileO) * col_tiles, kRowChunk);
   if (blocks == 0) return hipSuccess;
   hipLaunchKernelGGL((k_ffn_rows<T, B_KC, Epilogue>), tile_grid(blocks, kTileThreads),
                      dim3(kTileThreads), 0, s, g, static_cast<const T*>(a),
@@ -68,41 +89,59 @@ hipError_t rows_product(const Groups& g, const void* a, const void* b, int64_t K
   return hipGetLastError();
 }
 
-// out[e] = A' B over expert e's rows
-template <class T>
-hipError_t weights_product(const Groups& g, const void* a, const void* b, int64_t M, int64_t N,
-                           void* out, float* sums, hipStream_t s) {
-  const int64_t parts = weight_parts(g.rows, g.experts, M, N);
-  const uint32_t rt = (uint32_t)((M + kTileO - 1) / kTileO);
-  const uint32_t ct = (uint32_t)((N + kTileO - 1) / kTileO);
-  const dim3 grid =
-      tile_grid(blocks_of((int64_t)rt * ct * parts * g.experts), kTileThreads);
-  if (parts == 1) {
-    const StoreEpilogue<T> epilogue{static_cast<T*>(out), N, M * N};
-    hipLaunchKernelGGL((k_ffn_weights<T, StoreEpilogue<T>>), grid, dim3(kTileThreads), 0, s, g,
-                       static_cast<const T*>(a), static_cast<const T*>(b), M, N, rt, ct, 1u,
-                       epilogue);
-    return hipGetLastError();
+template <class T, class Out>
+hipError_t launch_weights(WeightProducts<T>& w, const WeightEpilogue<Out>& out, hipStream_t s) {
+  constexpr int WM = 2, WN = 4;
+  bool wide = sizeof(T) == 2;
+  for (int p = 0; p < 2; ++p)
+    wide = wide && w.M[p] % 8 == 0 && w.N[p] % 8 == 0 && on16(w.A[p]) && on16(w.B[p]);
+  const int64_t tile = wide ? kWideO : kTileO;
+  int64_t tiles = 0;
+  for (int p = 0; p < 2; ++p) {
+    w.row_tiles[p] = (uint32_t)((w.M[p] + tile - 1) / tile);
+    w.col_tiles[p] = (uint32_t)((w.N[p] + tile - 1) / tile);
+    tiles += (int64_t)w.row_tiles[p] * w.col_tiles[p];
   }
-  const PartEpilogue epilogue{sums, N, M * N};
-  hipLaunchKernelGGL((k_ffn_weights<T, PartEpilogue>), grid, dim3(kTileThreads), 0, s, g,
-                     static_cast<const T*>(a), static_cast<const T*>(b), M, N, rt, ct,
-                     (uint32_t)parts, epilogue);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int64_t vecs = (M * N + 3) / 4 * g.experts;
-  hipLaunchKernelGGL((k_ffn_add_parts<T>), row_grid((vecs + 255) / 256), dim3(256), 0, s, sums,
-                     (uint32_t)parts, M * N, g.experts, static_cast<T*>(out));
+  const int64_t blocks = blocks_of(tiles * w.parts * w.groups.experts, kWeightChunk);
+  if constexpr (sizeof(T) == 2) {
+    if (wide) {
+      hipLaunchKernelGGL((k_ffn_weights_wide<T, Out, WM, WN>), tile_grid(blocks, 64 * WM * WN),
+                         dim3(64 * WM * WN), 0, s, w, out);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((k_ffn_weights<T, Out>), tile_grid(blocks, kTileThreads), dim3(kTileThreads),
+                     0, s, w, out);
   return hipGetLastError();
+}
+
+// dw_in[e] = dgu' x and dw_out[e] = dy' a over expert e's rows
+template <class T>
+hipError_t weight_gradients(const Groups& g, const T* dgu, const void* x, const void* dy,
+                            const void* a, int64_t D, int64_t F, void* dw_in, void* dw_out,
+                            float* sums, hipStream_t s) {
+  const int64_t parts = weight_parts(g.rows, g.experts, D, F);
+  WeightProducts<T> w{g, {dgu, static_cast<const T*>(dy)},
+                      {static_cast<const T*>(x), static_cast<const T*>(a)},
+                      {2 * F, D}, {D, F}, {}, {}, (uint32_t)parts};
+  T* const out[2] = {static_cast<T*>(dw_in), static_cast<T*>(dw_out)};
+  if (parts == 1) return launch_weights(w, WeightEpilogue<T>{{out[0], out[1]}}, s);
+  float* const part[2] = {sums, sums + parts * g.experts * 2 * F * D};
+  hipError_t e = launch_weights(w, WeightEpilogue<float>{{part[0], part[1]}}, s);
+  for (int p = 0; p < 2 && e == hipSuccess; ++p) {
+    const int64_t vecs = (w.M[p] * w.N[p] + 3) / 4 * g.experts;
+    hipLaunchKernelGGL((k_ffn_add_parts<T>), row_grid((vecs + 255) / 256), dim3(256), 0, s,
+                       part[p], (uint32_t)parts, w.M[p] * w.N[p], g.experts, out[p]);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace
 
 template <class T>
 size_t ffn_workspace_bytes_t(int64_t rows, int32_t experts, int64_t dim, int64_t hidden) {
-  const size_t in = parts_bytes(rows, experts, 2 * hidden, dim);
-  const size_t out = parts_bytes(rows, experts, dim, hidden);
-  return dgu_bytes(rows, hidden, sizeof(T)) + (in > out ? in : out) + 256;
+  return dgu_bytes(rows, hidden, sizeof(T)) + parts_bytes(rows, experts, dim, hidden) + 256;
 }
 
 template <class T>
@@ -114,7 +153,7 @@ hipError_t ffn_forward_t(const GatedFfn& f, void* gu, void* a, void* y, char*, h
       ActEpilogue<T>{static_cast<T*>(gu), static_cast<T*>(a), F, f.act}, s);
   if (e != hipSuccess) return e;
   return rows_product<T, true>(g, a, f.w_out, F, D, D * F,
-                               StoreEpilogue<T>{static_cast<T*>(y), D, 0}, s);
+                               StoreEpilogue<T>{static_cast<T*>(y), D}, s);
 }
 
 template <class T>
@@ -129,11 +168,9 @@ hipError_t ffn_backward_t(const GatedFfn& f, const void* gu, const void* a, cons
       ActGradEpilogue<T>{static_cast<const T*>(gu), dgu, F, f.act}, s);
   if (e != hipSuccess) return e;
   e = rows_product<T, false>(g, dgu, f.w_in, 2 * F, D, 2 * F * D,
-                             StoreEpilogue<T>{static_cast<T*>(dx), D, 0}, s);
+                             StoreEpilogue<T>{static_cast<T*>(dx), D}, s);
   if (e != hipSuccess) return e;
-  e = weights_product<T>(g, dgu, f.x, 2 * F, D, dw_in, sums, s);
-  if (e != hipSuccess) return e;
-  return weights_product<T>(g, dy, a, D, F, dw_out, sums, s);
+  return weight_gradients<T>(g, dgu, f.x, dy, a, D, F, dw_in, dw_out, sums, s);
 }
 
 #define EMBTAB_FFN_TYPE(T)                                                                     \

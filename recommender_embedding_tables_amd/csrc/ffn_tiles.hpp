@@ -245,43 +245,36 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ffn_rows(
     for (int j = 0; j < (Epilogue::kDual ? 2 : 4); ++j) {
       const int64_t n = n0 + wn + j * 16 + (lane >> 4) * 4;
       if (n >= N) continue;
+      const typename Epilogue::Held held = epilogue.held(first + m, n);
       if constexpr (Epilogue::kDual)
-        epilogue(t.expert, first + m, n, acc[i][j], acc[i][j + 2]);
+        epilogue(first + m, n, acc[i][j], acc[i][j + 2], held);
       else
-        epilogue(t.expert, first + m, n, acc[i][j]);
+        epilogue(first + m, n, acc[i][j], held);
     }
   }
 }
 
-// Weight gradients: C[m, n] = sum over one expert's rows of A[row, m] B[row, n].
-// An expert's rows may be cut into `parts` (matrix e * parts + part of the output).
-template <class T, class Epilogue>
-__global__ __launch_bounds__(kTileThreads, 2) void k_ffn_weights(
-    const Groups groups, const T* __restrict__ A, const T* __restrict__ B, int64_t M, int64_t N,
-    uint32_t row_tiles, uint32_t col_tiles, uint32_t parts, const Epilogue epilogue) {
+// Weight gradients.
+template <class T, class Out>
+__global__ __launch_bounds__(kTileThreads, 2) void k_ffn_weights(const WeightProducts<T> w,
+                                                                 const WeightEpilogue<Out> out) {
   typedef TileProduct<T, false, false> Product;
   __shared__ __attribute__((aligned(16))) uint16_t lds[Product::kLds];
-  const uint32_t tiles = row_tiles * col_tiles;
-  uint64_t place;
-  if (!place_of(block_index(), (uint64_t)tiles * parts * groups.experts, place)) return;
-  const uint32_t matrix = (uint32_t)(place / tiles);
-  uint32_t rt, ct;
-  panel_tile((uint32_t)(place - (uint64_t)matrix * tiles), row_tiles, col_tiles, rt, ct);
-  const int32_t e = (int32_t)(matrix / parts);
-  const uint32_t part = matrix - (uint32_t)e * parts;
-  const Group g = group_of(groups, e);
-  // whole steps to each part
-  const int64_t per = ((g.count + parts - 1) / parts + kTileK - 1) / kTileK * kTileK;
-  const int64_t from = per * part < g.count ? per * part : g.count;
-  const int64_t K = g.count - from < per ? g.count - from : per;
-  const int64_t m0 = (int64_t)rt * kTileO, n0 = (int64_t)ct * kTileO;
+  WeightTile t;
+  if (!find_weight_tile(w, block_index(), t)) return;
+  const Group g = group_of(w.groups, t.expert);
+  int64_t from, K;
+  part_rows(g, w.parts, t.part, kTileK, from, K);
+  const int64_t M = w.M[t.product], N = w.N[t.product];
+  const int64_t m0 = (int64_t)t.rt * kTileO, n0 = (int64_t)t.ct * kTileO;
   Staged<T, false> a, b;
-  a.init_oc(A + (g.first + from) * M, M, m0, M);
-  b.init_oc(B + (g.first + from) * N, N, n0, N);
+  a.init_oc(w.A[t.product] + (g.first + from) * M, M, m0, M);
+  b.init_oc(w.B[t.product] + (g.first + from) * N, N, n0, N);
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
   const uint32_t wm = (wave & 1u) * 64u, wn = (wave >> 1) * 64u;
   f32x4 acc[4][4];
   Product::run(a, b, K, M, N, wm, [&](int j) { return wn + j * 16u; }, lds, acc);
+  const int64_t matrix = (int64_t)t.expert * w.parts + t.part;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t m = m0 + wm + i * 16 + (lane & 15u);
@@ -289,7 +282,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ffn_weights(
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t n = n0 + wn + j * 16 + (lane >> 4) * 4;
-      if (n < N) epilogue((int32_t)matrix, m, n, acc[i][j]);
+      if (n < N) out(t.product, matrix, M, N, m, n, acc[i][j]);
     }
   }
 }
