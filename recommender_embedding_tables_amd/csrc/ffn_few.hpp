@@ -1,0 +1,162 @@
+// Grouped matrix products of few rows (serving): the weights' bytes bound them,
+// for gfx950.
+//
+// C[m, n] = sum_k A(m, k) B(n, k), both with k innermost.  A block takes 16
+// columns (of both projections for a dual epilogue) of up to 64 rows of one
+// expert, so that a weight is read once for all of them, and its four waves take
+// turns in k; their sums are added in order through LDS.  Nothing else passes
+// through LDS: a fragment of a matrix instruction is 16 or 32 neighbouring bytes
+// of a row, in any order of k as long as both operands share it, so a lane loads
+// its own, and the four lanes of a row read a line together.  fp32 takes the fp32
+// matrix instructions, which keep up with the memory at these rows.
+#pragma once
+
+#include "ffn.hpp"
+
+namespace embtab {
+
+constexpr int kFewRows = 64, kFewCols = 16, kFewWaves = 4;
+
+template <class T>
+struct FewStep {
+  // k values of a step, and 16-byte vectors of a lane's part of it
+  static constexpr int kVecs = sizeof(T) == 2 ? 2 : 1;
+  static constexpr int kLane = kVec<T> * kVecs, kK = 4 * kLane;
+  Raw<T> r[kVecs];
+
+  // k0 .. of K, from a row's first value
+  __device__ inline void load(const T* row, uint32_t k, int32_t K) {
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const int32_t at = (int32_t)k + v * kVec<T>;
+      if (at + kVec<T> <= K) {
+        r[v] = load_raw(row + at);
+      } else {
+        float f[kVec<T>];
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e) f[e] = at + e < K ? to_f32(row[at + e]) : 0.0f;
+        r[v].set_all(f);
+      }
+    }
+  }
+  static __device__ inline f32x4 product(const FewStep& b, const FewStep& a, f32x4 c) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v)
+        c = mfma_16x16x32<T>(__builtin_bit_cast(i16x8, b.r[v]), __builtin_bit_cast(i16x8, a.r[v]),
+                             c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(b.r[0].get(e), a.r[0].get(e), c, 0, 0, 0);
+    }
+    return c;
+  }
+};
+
+// The wave's sums of MT x 16 rows and COLS sets of 16 columns.
+template <class T, int MT, int COLS>
+__device__ inline void few_sums(const T* const (&a)[MT], const T* const (&b)[COLS], int32_t K,
+                                uint32_t wave, uint32_t q, f32x4 (&acc)[MT][COLS]) {
+  typedef FewStep<T> Step;
+  constexpr int kAhead = MT >= 4 ? 2 : 4;  // steps whose loads are under way together
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) acc[i][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const uint32_t lane_k = q * Step::kLane;
+  int32_t k0 = wave * Step::kK;
+  constexpr int32_t kTurn = kFewWaves * Step::kK;
+  for (; k0 + (kAhead - 1) * kTurn + Step::kK <= K; k0 += kAhead * kTurn) {
+    Step sa[kAhead][MT], sb[kAhead][COLS];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+#pragma unroll
+      for (int c = 0; c < COLS; ++c)
+#pragma unroll
+        for (int v = 0; v < Step::kVecs; ++v)
+          sb[s][c].r[v] = load_raw<T, kVec<T>, true>(b[c] + k0 + s * kTurn + lane_k + v * kVec<T>);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int v = 0; v < Step::kVecs; ++v)
+          sa[s][i].r[v] = load_raw(a[i] + k0 + s * kTurn + lane_k + v * kVec<T>);
+    }
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) acc[i][c] = Step::product(sb[s][c], sa[s][i], acc[i][c]);
+  }
+  for (; k0 < K; k0 += kTurn) {
+    Step sa[MT], sb[COLS];
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) sb[c].load(b[c], k0 + lane_k, K);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sa[i].load(a[i], k0 + lane_k, K);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) acc[i][c] = Step::product(sb[c], sa[i], acc[i][c]);
+  }
+}
+
+template <class T, int MT, class Epilogue>
+__device__ inline void few_rows(const RowTile& t, const T* __restrict__ A,
+                                const T* __restrict__ B, int32_t K, int64_t N, int64_t b_stride,
+                                const Epilogue& epilogue, f32x4* lds) {
+  constexpr int COLS = Epilogue::kDual ? 2 : 1;
+  const uint32_t lane = threadIdx.x & 63u, q = lane >> 4, i16 = lane & 15u;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m0 = (int64_t)t.rt * kFewRows, n0 = (int64_t)t.ct * kFewCols;
+  const int64_t last = t.count - 1 - m0, last_n = N - 1 - n0;
+  const T *a[MT], *b[COLS];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t m = i * 16 + i16;
+    a[i] = A + (t.first + m0 + (m < last ? m : last)) * K;
+  }
+#pragma unroll
+  for (int c = 0; c < COLS; ++c)
+    b[c] = B + t.expert * b_stride + (n0 + ((int64_t)i16 < last_n ? i16 : last_n) + c * N) * K;
+  f32x4 acc[MT][COLS];
+  few_sums<T, MT, COLS>(a, b, K, wave, q, acc);
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) lds[((wave * MT + i) * COLS + c) * 64 + lane] = acc[i][c];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    if (i % kFewWaves != (int)wave) continue;
+    f32x4 sum[COLS];
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) {
+      sum[c] = lds[(i * COLS + c) * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < kFewWaves; ++w) sum[c] += lds[((w * MT + i) * COLS + c) * 64 + lane];
+    }
+    const int64_t m = m0 + i * 16 + i16, n = n0 + q * 4;
+    if (m >= t.count || n >= N) continue;
+    if constexpr (Epilogue::kDual)
+      epilogue(t.first + m, n, sum[0], sum[1], {});
+    else
+      epilogue(t.first + m, n, sum[0], {});
+  }
+}
+
+template <class T, class Epilogue>
+__global__ __launch_bounds__(64 * kFewWaves) void k_ffn_few_rows(
+    const Groups groups, const T* __restrict__ A, const T* __restrict__ B, int32_t K, int64_t N,
+    int64_t b_stride, uint32_t col_tiles, const Epilogue epilogue) {
+  __shared__ f32x4 lds[kFewWaves * 4 * (Epilogue::kDual ? 2 : 1) * 64];
+  RowTile t;
+  if (!find_row_tile(groups, kFewRows, col_tiles, block_index(), t)) return;
+  const int64_t rows = t.count - (int64_t)t.rt * kFewRows;
+  if (rows <= 16) few_rows<T, 1>(t, A, B, K, N, b_stride, epilogue, lds);
+  else if (rows <= 32) few_rows<T, 2>(t, A, B, K, N, b_stride, epilogue, lds);
+  else few_rows<T, 4>(t, A, B, K, N, b_stride, epilogue, lds);
+}
+
+}  // namespace embtab

@@ -2,6 +2,7 @@
 // one source per type).
 #pragma once
 
+#include "ffn_few.hpp"
 #include "ffn_wide.hpp"
 
 namespace embtab {
@@ -61,17 +62,37 @@ __global__ __launch_bounds__(256) void k_ffn_add_parts(const float* __restrict__
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+#ifndef FEW
+#define FEW 64
+#endif
+// C = A B' over groups of few rows
+template <class T, class Epilogue>
+hipError_t few_rows_product(const Groups& g, const void* a, const void* b, int64_t K, int64_t N,
+                            int64_t b_stride, const Epilogue& epilogue, hipStream_t s) {
+  const int64_t col_tiles = (N + kFewCols - 1) / kFewCols;
+  const int64_t blocks = blocks_of(row_tiles_bound(g, kFewRows) * col_tiles, kRowChunk);
+  hipLaunchKernelGGL((k_ffn_few_rows<T, Epilogue>), tile_grid(blocks, 64 * kFewWaves),
+                     dim3(64 * kFewWaves), 0, s, g, static_cast<const T*>(a),
+                     static_cast<const T*>(b), (int32_t)K, N, b_stride, (uint32_t)col_tiles,
+                     epilogue);
+  return hipGetLastError();
+}
+
 // C = A B' or A B (B_KC) over the groups' rows
 template <class T, bool B_KC, class Epilogue>
 hipError_t rows_product(const Groups& g, const void* a, const void* b, int64_t K, int64_t N,
                         int64_t b_stride, const Epilogue& epilogue, hipStream_t s) {
+  if (g.rows == 0) return hipSuccess;
+  if constexpr (B_KC) {
+    if (g.rows <= FEW * (int64_t)g.experts)
+      return few_rows_product<T>(g, a, b, K, N, b_stride, epilogue, s);
+  }
   if constexpr (sizeof(T) == 2) {
     if (K % 8 == 0 && (B_KC || N % 8 == 0) && on16(a) && on16(b)) {
       constexpr int WM = 2, WN = 4;
       const int64_t cols = Epilogue::kDual ? kWideO / 2 : kWideO;
       const int64_t col_tiles = (N + cols - 1) / cols;
       const int64_t blocks = blocks_of(row_tiles_bound(g, kWideO) * col_tiles, kRowChunk);
-      if (blocks == 0) return hipSuccess;
       hipLaunchKernelGGL((k_ffn_rows_wide<T, B_KC, Epilogue, WM, WN>),
                          tile_grid(blocks, 64 * WM * WN), dim3(64 * WM * WN), 0, s, g,
                          static_cast<const T*>(a), static_cast<const T*>(b), K, N, b_stride,
@@ -82,7 +103,6 @@ hipError_t rows_product(const Groups& g, const void* a, const void* b, int64_t K
   const int64_t cols = Epilogue::kDual ? kTileO / 2 : kTileO;
   const int64_t col_tiles = (N + cols - 1) / cols;
   const int64_t blocks = blocks_of(row_tiles_bound(g, kTileO) * col_tiles, kRowChunk);
-  if (blocks == 0) return hipSuccess;
   hipLaunchKernelGGL((k_ffn_rows<T, B_KC, Epilogue>), tile_grid(blocks, kTileThreads),
                      dim3(kTileThreads), 0, s, g, static_cast<const T*>(a),
                      static_cast<const T*>(b), K, N, b_stride, (uint32_t)col_tiles, epilogue);

@@ -27,11 +27,13 @@ constexpr int kTileO = 128, kTileK = 32, kTileThreads = 256;
 template <class T>
 constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
 
-// A KC plane has rows of 32 values 80 bytes apart, an OC plane rows of 128 in
-// turned 32-byte pieces: both are read without bank conflicts.
-constexpr int kKcStride = 40;
-constexpr int kPlaneValues = kTileO * kKcStride;  // OC: 32 * 128, less
+// A KC plane has rows of 32 values, an OC plane rows of 128.  The four 16-byte
+// pieces of a KC row are turned so that the 16 lanes that a 16-byte read serves at
+// once (rows 0 to 3 and 12 to 15 of one piece with 4 to 11 of the next) meet no
+// bank twice, the 32-byte pieces of an OC row so that eight rows of 32 bytes do not.
+constexpr int kPlaneValues = kTileO * kTileK;
 
+__device__ inline uint32_t kc_turn(uint32_t row) { return (row & 8u) ? 3u : 0u; }
 __device__ inline uint32_t oc_turn(uint32_t k) { return ((k & 3u) | ((k >> 1) & 4u)) << 1; }
 
 // One operand's share of a thread: its vectors of a tile, loaded and written.
@@ -42,6 +44,7 @@ struct Staged {
   static constexpr int kPer = (KC ? kTileK : kTileO) / V;  // vectors of a tile's row
   const T* p[kVecs];
   int32_t have[kVecs];  // OC: values of the vector inside the matrix
+  bool whole;           // OC: the tile lies inside it
   Raw<T> r[kVecs];
 
   // row(i): memory offset of the operand's index i of the tile (KC)
@@ -55,6 +58,7 @@ struct Staged {
   }
   // index o0 .. of `limit`, rows of ld values (OC)
   __device__ inline void init_oc(const T* base, int64_t ld, int64_t o0, int64_t limit) {
+    whole = o0 + kTileO <= limit;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const uint32_t v = threadIdx.x + i * kTileThreads;
@@ -74,8 +78,14 @@ struct Staged {
     return x;
   }
 
-  // k0 .. of K; ld as in init_oc
+  // k0 .. of K; ld as in init_oc.  A step inside the matrix takes no branch for
+  // each vector, at whose end the compiler would wait for the load.
   __device__ inline void load(int64_t k0, int64_t K, int64_t ld) {
+    if (k0 + kTileK <= K && (KC || whole)) {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) r[i] = load_raw(p[i] + (KC ? k0 : k0 * ld));
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const uint32_t v = threadIdx.x + i * kTileThreads;
@@ -96,7 +106,7 @@ struct Staged {
     for (int i = 0; i < kVecs; ++i) {
       const uint32_t v = threadIdx.x + i * kTileThreads;
       const uint32_t row = v / kPer, c = (v % kPer) * V;
-      const uint32_t at = KC ? row * kKcStride + c
+      const uint32_t at = KC ? row * kTileK + (((c >> 3) ^ kc_turn(row)) << 3) + (c & 7u)
                              : row * kTileO + (((c >> 3) ^ oc_turn(row)) << 3) + (c & 7u);
       if constexpr (sizeof(T) == 2) {
         *reinterpret_cast<u4*>(lds + at) = u4{r[i].w[0], r[i].w[1], r[i].w[2], r[i].w[3]};
@@ -104,13 +114,14 @@ struct Staged {
         uint32_t words[3][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float a = r[i].get(2 * h), b = r[i].get(2 * h + 1);
+          f32x2 v = {r[i].get(2 * h), r[i].get(2 * h + 1)};
 #pragma unroll
           for (int q = 0; q < 3; ++q) {
-            const uint32_t lo = from_f32<bf16_t>(a).bits, hi = from_f32<bf16_t>(b).bits;
-            words[q][h] = lo | (hi << 16);
-            a -= __uint_as_float(lo << 16);
-            b -= __uint_as_float(hi << 16);
+            const uint32_t w =
+                __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+            words[q][h] = w;
+            v[0] -= __uint_as_float(w << 16);
+            v[1] -= __uint_as_float(w & 0xFFFF0000u);
           }
         }
 #pragma unroll
@@ -125,7 +136,8 @@ struct Staged {
 template <bool KC>
 __device__ inline i16x8 tile_fragment(const uint16_t* lds, uint32_t o0, uint32_t lane) {
   const uint32_t i = lane & 15u, q = lane >> 4;
-  if (KC) return *reinterpret_cast<const i16x8*>(lds + (o0 + i) * kKcStride + q * 8);
+  if (KC)
+    return *reinterpret_cast<const i16x8*>(lds + (o0 + i) * kTileK + ((q ^ kc_turn(i)) << 3));
   i16x4 h[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {

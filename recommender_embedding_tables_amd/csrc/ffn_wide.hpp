@@ -15,11 +15,6 @@ constexpr int kStageValues = 2 * kWideValues;
 // Sixteen bytes of zeros that vectors past the end are taken from.
 __device__ const uint32_t kZeroVector[4] = {0u, 0u, 0u, 0u};
 
-// The four 16-byte pieces of a KC row of 64 bytes are turned so that the 16 lanes
-// that a 16-byte read serves at once (rows 0 to 3 and 12 to 15 of one piece with
-// 4 to 11 of the next) meet no bank twice.
-__device__ inline uint32_t kc_turn(uint32_t row) { return (row & 8u) ? 3u : 0u; }
-
 // Loads of one operand straight into LDS: THREADS threads, kVecs vectors each a
 // stage.  The place of a vector in LDS is the thread's own (the hardware puts a
 // wave's 64 vectors one after another), so the turning that keeps the reads free
