@@ -306,8 +306,7 @@ struct ActEpilogue {
   int32_t act;
   typedef NothingHeld Held;
   __device__ inline Held held(int64_t, int64_t) const { return {}; }
-  __device__ inline void operator()(int64_t row, int64_t n, f32x4 g, f32x4 u,
-                                    Held) const {
+  __device__ inline f32x4 product(int64_t row, int64_t n, f32x4 g, f32x4 u) const {
     const int64_t have = width - n;
     if (gu) {
       store4(gu + row * 2 * width + n, g, have);
@@ -317,6 +316,10 @@ struct ActEpilogue {
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = act_value<T>(act, g[i]).a * u[i];
     store4(a + row * width + n, p, have);
+    return p;
+  }
+  __device__ inline void operator()(int64_t row, int64_t n, f32x4 g, f32x4 u, Held) const {
+    product(row, n, g, u);
   }
 };
 
@@ -335,21 +338,18 @@ struct ActGradEpilogue {
     return {load_part4(gu + row * 2 * width + n, width - n),
             load_part4(gu + (row * 2 + 1) * width + n, width - n)};
   }
-  __device__ inline void operator()(int64_t row, int64_t n, f32x4 da,
-                                    const Held& h) const {
-    const int64_t have = width - n;
-    f32x4 g, u, dg, du;
+  __device__ inline void gradients(f32x4 da, const Held& h, f32x4& dg, f32x4& du) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      g[i] = h.g.get(i);
-      u[i] = h.u.get(i);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const ActValue f = act_value<T>(act, g[i]);
-      dg[i] = da[i] * u[i] * f.slope;
+      const ActValue f = act_value<T>(act, h.g.get(i));
+      dg[i] = da[i] * h.u.get(i) * f.slope;
       du[i] = da[i] * f.a;
     }
+  }
+  __device__ inline void operator()(int64_t row, int64_t n, f32x4 da, const Held& h) const {
+    const int64_t have = width - n;
+    f32x4 dg, du;
+    gradients(da, h, dg, du);
     store4(dgu + row * 2 * width + n, dg, have);
     store4(dgu + (row * 2 + 1) * width + n, du, have);
   }

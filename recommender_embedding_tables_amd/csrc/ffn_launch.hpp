@@ -3,7 +3,7 @@
 #pragma once
 
 #include "ffn_few.hpp"
-#include "ffn_wide.hpp"
+#include "ffn_planes.hpp"
 
 namespace embtab {
 
@@ -109,8 +109,64 @@ hipError_t rows_product(const Groups& g, const void* a, const void* b, int64_t K
   return hipGetLastError();
 }
 
+#ifndef ONEROUND
+#define ONEROUND 192
+#endif
+#ifndef PLANES
+#define PLANES 128
+#endif
+// fp32 goes through planes where an expert has this many rows: its values then
+// enter more than one tile.
+bool by_planes(int64_t rows, int32_t experts) { return rows >= PLANES * (int64_t)experts; }
+
+// Hands out the workspace from its start.
+struct Space {
+  char* at;
+  Planes planes(int64_t rows, int64_t width) {
+    const Planes p{reinterpret_cast<bf16_t*>(at), padded(width), rows * padded(width)};
+    at += align256((size_t)p.size * 6);
+    return p;
+  }
+};
+size_t planes_bytes(int64_t rows, int64_t width) {
+  return align256((size_t)rows * padded(width) * 6);
+}
+
+struct Cutter {
+  Cuts c{};
+  void add(const void* src, const Planes& dst, int64_t width) {
+    const int i = c.count++;
+    c.src[i] = static_cast<const float*>(src);
+    c.dst[i] = dst;
+    c.width[i] = width;
+    c.first[i + 1] = c.first[i] + dst.size / 8;
+  }
+  hipError_t launch(hipStream_t s) const {
+    hipLaunchKernelGGL(k_ffn_cut, row_grid((c.first[c.count] + 255) / 256), dim3(256), 0, s, c);
+    return hipGetLastError();
+  }
+};
+
+template <bool B_KC, class Epilogue>
+hipError_t rows_product_planes(const Groups& g, const Planes& a, const Planes& b, int64_t N,
+                               int64_t b_rows, const Epilogue& epilogue, hipStream_t s) {
+  const int64_t cols = Epilogue::kDual ? kTileO / 2 : kTileO;
+  const int64_t col_tiles = (N + cols - 1) / cols;
+  const int64_t blocks = blocks_of(row_tiles_bound(g, 128) * col_tiles, kRowChunk);
+  if (blocks <= ONEROUND) {
+    const int64_t half = blocks_of(row_tiles_bound(g, 64) * col_tiles, kRowChunk);
+    hipLaunchKernelGGL((k_ffn_rows_planes<B_KC, Epilogue, 64>), tile_grid(half, 256), dim3(256),
+                       0, s, g, a, b, N, b_rows, (uint32_t)col_tiles, epilogue);
+  } else {
+    hipLaunchKernelGGL((k_ffn_rows_planes<B_KC, Epilogue, 128>), tile_grid(blocks, 512), dim3(512),
+                       0, s, g, a, b, N, b_rows, (uint32_t)col_tiles, epilogue);
+  }
+  return hipGetLastError();
+}
+
 template <class T, class Out>
-hipError_t launch_weights(WeightProducts<T>& w, const WeightEpilogue<Out>& out, hipStream_t s) {
+hipError_t launch_weights(WeightProducts<T>& w, const WeightPlanes* planes,
+                          const WeightEpilogue<Out>& out, hipStream_t s) {
   constexpr int WM = 2, WN = 4;
   bool wide = sizeof(T) == 2;
   for (int p = 0; p < 2; ++p)
@@ -129,6 +185,10 @@ hipError_t launch_weights(WeightProducts<T>& w, const WeightEpilogue<Out>& out, 
                          dim3(64 * WM * WN), 0, s, w, out);
       return hipGetLastError();
     }
+  } else if (planes) {
+    hipLaunchKernelGGL((k_ffn_weights_planes<Out, 128>), tile_grid(blocks, 512), dim3(512), 0, s,
+                       w, *planes, out);
+    return hipGetLastError();
   }
   hipLaunchKernelGGL((k_ffn_weights<T, Out>), tile_grid(blocks, kTileThreads), dim3(kTileThreads),
                      0, s, w, out);
@@ -138,16 +198,16 @@ hipError_t launch_weights(WeightProducts<T>& w, const WeightEpilogue<Out>& out, 
 // dw_in[e] = dgu' x and dw_out[e] = dy' a over expert e's rows
 template <class T>
 hipError_t weight_gradients(const Groups& g, const T* dgu, const void* x, const void* dy,
-                            const void* a, int64_t D, int64_t F, void* dw_in, void* dw_out,
-                            float* sums, hipStream_t s) {
+                            const void* a, const WeightPlanes* planes, int64_t D, int64_t F,
+                            void* dw_in, void* dw_out, float* sums, hipStream_t s) {
   const int64_t parts = weight_parts(g.rows, g.experts, D, F);
   WeightProducts<T> w{g, {dgu, static_cast<const T*>(dy)},
                       {static_cast<const T*>(x), static_cast<const T*>(a)},
                       {2 * F, D}, {D, F}, {}, {}, (uint32_t)parts};
   T* const out[2] = {static_cast<T*>(dw_in), static_cast<T*>(dw_out)};
-  if (parts == 1) return launch_weights(w, WeightEpilogue<T>{{out[0], out[1]}}, s);
+  if (parts == 1) return launch_weights(w, planes, WeightEpilogue<T>{{out[0], out[1]}}, s);
   float* const part[2] = {sums, sums + parts * g.experts * 2 * F * D};
-  hipError_t e = launch_weights(w, WeightEpilogue<float>{{part[0], part[1]}}, s);
+  hipError_t e = launch_weights(w, planes, WeightEpilogue<float>{{part[0], part[1]}}, s);
   for (int p = 0; p < 2 && e == hipSuccess; ++p) {
     const int64_t vecs = (w.M[p] * w.N[p] + 3) / 4 * g.experts;
     hipLaunchKernelGGL((k_ffn_add_parts<T>), row_grid((vecs + 255) / 256), dim3(256), 0, s,
@@ -157,15 +217,72 @@ hipError_t weight_gradients(const Groups& g, const T* dgu, const void* x, const 
   return e;
 }
 
+// The forward and backward of fp32 through planes.
+hipError_t forward_planes(const GatedFfn& f, void* gu, void* a, void* y, char* ws,
+                          hipStream_t s) {
+  const int64_t D = f.dim, F = f.hidden;
+  const Groups g{f.offsets, f.rows, f.capacity, f.experts};
+  Space space{ws};
+  const Planes px = space.planes(f.rows, D), pa = space.planes(f.rows, F);
+  const Planes pin = space.planes(f.experts * 2 * F, D), pout = space.planes(f.experts * D, F);
+  Cutter cut;
+  cut.add(f.x, px, D);
+  cut.add(f.w_in, pin, D);
+  cut.add(f.w_out, pout, F);
+  hipError_t e = cut.launch(s);
+  if (e != hipSuccess) return e;
+  e = rows_product_planes<true>(
+      g, px, pin, F, 2 * F,
+      ActPlanesEpilogue{{static_cast<float*>(gu), static_cast<float*>(a), F, f.act}, pa}, s);
+  if (e != hipSuccess) return e;
+  return rows_product_planes<true>(g, pa, pout, D, D,
+                                   StorePlanesEpilogue{{static_cast<float*>(y), D}}, s);
+}
+
+hipError_t backward_planes(const GatedFfn& f, const void* gu, const void* a, const void* dy,
+                           void* dx, void* dw_in, void* dw_out, char* ws, hipStream_t s) {
+  const int64_t D = f.dim, F = f.hidden;
+  const Groups g{f.offsets, f.rows, f.capacity, f.experts};
+  Space space{ws};
+  const Planes px = space.planes(f.rows, D), pa = space.planes(f.rows, F);
+  const Planes pin = space.planes(f.experts * 2 * F, D), pout = space.planes(f.experts * D, F);
+  const Planes pdy = space.planes(f.rows, D), pdgu = space.planes(f.rows, 2 * F);
+  Cutter cut;
+  cut.add(f.x, px, D);
+  cut.add(a, pa, F);
+  cut.add(f.w_in, pin, D);
+  cut.add(f.w_out, pout, F);
+  cut.add(dy, pdy, D);
+  hipError_t e = cut.launch(s);
+  if (e != hipSuccess) return e;
+  e = rows_product_planes<false>(
+      g, pdy, pout, F, D,
+      ActGradPlanesEpilogue{{static_cast<const float*>(gu), nullptr, F, f.act}, pdgu}, s);
+  if (e != hipSuccess) return e;
+  e = rows_product_planes<false>(g, pdgu, pin, D, 2 * F,
+                                 StorePlanesEpilogue{{static_cast<float*>(dx), D}}, s);
+  if (e != hipSuccess) return e;
+  const WeightPlanes planes{{pdgu, pdy}, {px, pa}};
+  return weight_gradients<float>(g, nullptr, f.x, dy, a, &planes, D, F, dw_in, dw_out,
+                                 reinterpret_cast<float*>(space.at), s);
+}
+
 }  // namespace
 
 template <class T>
 size_t ffn_workspace_bytes_t(int64_t rows, int32_t experts, int64_t dim, int64_t hidden) {
-  return dgu_bytes(rows, hidden, sizeof(T)) + parts_bytes(rows, experts, dim, hidden) + 256;
+  size_t n = dgu_bytes(rows, hidden, sizeof(T));
+  if (sizeof(T) == 4 && by_planes(rows, experts))
+    n = 2 * planes_bytes(rows, dim) + planes_bytes(rows, hidden) +
+        planes_bytes(rows, 2 * hidden) + planes_bytes(experts * 2 * hidden, dim) +
+        planes_bytes(experts * dim, hidden);
+  return n + parts_bytes(rows, experts, dim, hidden) + 256;
 }
 
 template <class T>
-hipError_t ffn_forward_t(const GatedFfn& f, void* gu, void* a, void* y, char*, hipStream_t s) {
+hipError_t ffn_forward_t(const GatedFfn& f, void* gu, void* a, void* y, char* ws, hipStream_t s) {
+  if constexpr (sizeof(T) == 4)
+    if (by_planes(f.rows, f.experts)) return forward_planes(f, gu, a, y, ws, s);
   const int64_t D = f.dim, F = f.hidden;
   const Groups g{f.offsets, f.rows, f.capacity, f.experts};
   const hipError_t e = rows_product<T, true>(
@@ -179,6 +296,9 @@ hipError_t ffn_forward_t(const GatedFfn& f, void* gu, void* a, void* y, char*, h
 template <class T>
 hipError_t ffn_backward_t(const GatedFfn& f, const void* gu, const void* a, const void* dy,
                           void* dx, void* dw_in, void* dw_out, char* ws, hipStream_t s) {
+  if constexpr (sizeof(T) == 4)
+    if (by_planes(f.rows, f.experts))
+      return backward_planes(f, gu, a, dy, dx, dw_in, dw_out, ws, s);
   const int64_t D = f.dim, F = f.hidden;
   const Groups g{f.offsets, f.rows, f.capacity, f.experts};
   T* dgu = reinterpret_cast<T*>(ws);
@@ -190,7 +310,7 @@ hipError_t ffn_backward_t(const GatedFfn& f, const void* gu, const void* a, cons
   e = rows_product<T, false>(g, dgu, f.w_in, 2 * F, D, 2 * F * D,
                              StoreEpilogue<T>{static_cast<T*>(dx), D}, s);
   if (e != hipSuccess) return e;
-  return weight_gradients<T>(g, dgu, f.x, dy, a, D, F, dw_in, dw_out, sums, s);
+  return weight_gradients<T>(g, dgu, f.x, dy, a, nullptr, D, F, dw_in, dw_out, sums, s);
 }
 
 #define EMBTAB_FFN_TYPE(T)                                                                     \

@@ -1,0 +1,342 @@
+// Grouped matrix products of fp32 values that are cut into three bf16 planes
+// before, for gfx950.
+//
+// The tiles of ffn_tiles.hpp cut an fp32 value into bf16 each time it enters a
+// tile, which costs a vector instruction for every matrix instruction's cycle.
+// Where a value enters several tiles its planes are made once instead (6 bytes a
+// value, rows padded with zeros to a multiple of 8, so that any width and
+// alignment will do), the products' results leave theirs as they are stored, and
+// the tiles load planes straight into LDS.  The six products and their order are
+// those of ffn_tiles.hpp.
+#pragma once
+
+#include "ffn_wide.hpp"
+
+namespace embtab {
+
+__host__ __device__ inline int64_t padded(int64_t n) { return (n + 7) & ~(int64_t)7; }
+
+// An fp32 matrix's planes: [3][rows][ld] bf16.
+struct Planes {
+  bf16_t* p;
+  int64_t ld, size;  // values of a row, of a plane
+};
+
+__device__ inline void cut_planes(float a, float b, uint32_t (&w)[3]) {
+  f32x2 v = {a, b};
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    w[q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+    v[0] -= __uint_as_float(w[q] << 16);
+    v[1] -= __uint_as_float(w[q] & 0xFFFF0000u);
+  }
+}
+
+// The planes of the first `have` of four values, then zeros up to `to` of them.
+__device__ inline void store_planes4(const Planes& o, int64_t at, f32x4 v, int64_t have,
+                                     int64_t to) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = i < have ? v[i] : 0.0f;
+  uint32_t lo[3], hi[3];
+  cut_planes(v[0], v[1], lo);
+  cut_planes(v[2], v[3], hi);
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(o.p) + q * o.size + at;
+    if (to >= 4) {
+      *reinterpret_cast<u2_at2*>(p) = u2{lo[q], hi[q]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < to) p[i] = (uint16_t)((i < 2 ? lo[q] : hi[q]) >> (16 * (i & 1)));
+    }
+  }
+}
+
+// Matrices cut in one launch.
+constexpr int kMaxCuts = 5;
+struct Cuts {
+  const float* src[kMaxCuts];
+  Planes dst[kMaxCuts];
+  int64_t width[kMaxCuts];
+  int64_t first[kMaxCuts + 1];  // vectors of 8 values before each matrix
+  int32_t count;
+};
+
+__global__ __launch_bounds__(256) inline void k_ffn_cut(const Cuts c) {
+  const int64_t v = (int64_t)block_index() * 256 + threadIdx.x;
+  if (v >= c.first[c.count]) return;
+  int m = 0;
+#pragma unroll
+  for (int i = 1; i < kMaxCuts; ++i) m += i < c.count && v >= c.first[i];
+  const float* src = c.src[0];
+  Planes dst = c.dst[0];
+  int64_t width = c.width[0], first = 0;
+#pragma unroll
+  for (int i = 1; i < kMaxCuts; ++i)
+    if (i == m) {
+      src = c.src[i];
+      dst = c.dst[i];
+      width = c.width[i];
+      first = c.first[i];
+    }
+  const int64_t per = dst.ld / 8, row = (v - first) / per, col = (v - first - row * per) * 8;
+  const float* p = src + row * width + col;
+  float f[8];
+  if (col + 8 <= width) {
+    const Raw<float> a = load_raw(p), b = load_raw(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = a.get(i);
+      f[4 + i] = b.get(i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = col + i < width ? p[i] : 0.0f;
+  }
+  uint32_t w[4][3];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) cut_planes(f[2 * i], f[2 * i + 1], w[i]);
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
+    *reinterpret_cast<u4*>(dst.p + q * dst.size + row * dst.ld + col) =
+        u4{w[0][q], w[1][q], w[2][q], w[3][q]};
+}
+
+// ---------------------------------------------------------------- epilogues
+// Both also cover the columns that pad a row of planes.
+struct ActPlanesEpilogue {
+  static constexpr bool kDual = true;
+  ActEpilogue<float> values;
+  Planes a;
+  __device__ inline int64_t columns() const { return a.ld; }
+  typedef NothingHeld Held;
+  __device__ inline Held held(int64_t, int64_t) const { return {}; }
+  __device__ inline void operator()(int64_t row, int64_t n, f32x4 g, f32x4 u, Held) const {
+    const int64_t have = values.width - n;
+    const f32x4 p = values.product(row, n, g, u);
+    store_planes4(a, row * a.ld + n, p, have, a.ld - n);
+  }
+};
+
+struct ActGradPlanesEpilogue {
+  static constexpr bool kDual = false;
+  ActGradEpilogue<float> values;  // its dgu is not written
+  Planes dgu;
+  __device__ inline int64_t columns() const { return values.width + dgu.ld - 2 * values.width; }
+  typedef ActGradEpilogue<float>::Held Held;
+  __device__ inline Held held(int64_t row, int64_t n) const { return values.held(row, n); }
+  __device__ inline void operator()(int64_t row, int64_t n, f32x4 da, const Held& h) const {
+    const int64_t width = values.width, have = width - n;
+    f32x4 dg, du;
+    values.gradients(da, h, dg, du);
+    store_planes4(dgu, row * dgu.ld + n, dg, have, have);
+    store_planes4(dgu, row * dgu.ld + width + n, du, have, dgu.ld - width - n);
+  }
+};
+
+struct StorePlanesEpilogue : StoreEpilogue<float> {
+  __device__ inline int64_t columns() const { return width; }
+};
+
+// ---------------------------------------------------------------- product
+// Tiles of OM x 128 by waves of 64 x 32: 128 rows by eight waves and a ring of
+// three stages, 64 rows by four and a ring of four (144 KB of LDS either way).  A
+// stage holds 32 k of both operands' planes.
+template <bool A_KC, bool B_KC, int OM>
+struct PlaneProduct {
+  static constexpr int WM = OM / 64, WN = 4, kThreads = 64 * WM * WN, kRing = OM == 128 ? 3 : 4;
+  static constexpr int FM = 4, FN = 2;
+  typedef StageLoads<A_KC, OM, kThreads> LoadsA;
+  typedef StageLoads<B_KC, kTileO, kThreads> LoadsB;
+  static constexpr int kLoads = 3 * (LoadsA::kVecs + LoadsB::kVecs);
+  static constexpr uint32_t kPlaneA = OM * kWideK * 2, kPlaneB = kTileO * kWideK * 2;
+  static constexpr uint32_t kStage = 3 * (kPlaneA + kPlaneB);
+
+  // size_a, size_b: bytes of a plane
+  template <class Delta>
+  __device__ static inline void run(LoadsA& a, LoadsB& b, int64_t step_a, int64_t step_b,
+                                    int64_t size_a, int64_t size_b, int32_t stages,
+                                    const Fragments<A_KC, OM>& at_a,
+                                    const Fragments<B_KC, kTileO>& at_b, Delta delta_b,
+                                    uint16_t* lds, f32x4 (&acc)[FM][FN]) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (stages <= 0) return;
+    const uint32_t ring = lds_address(lds);
+    const uint32_t mine = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+    const auto issue = [&](int load, uint32_t stage) {  // of kLoads: a's vectors, then b's
+      if (load < 3 * LoadsA::kVecs) {
+        const int q = load % 3, l = load / 3;
+        a.issue(l, stage + mine + q * kPlaneA, q * size_a);
+        if (q == 2) a.advance(l, step_a);
+      } else {
+        const int q = load % 3, l = load / 3 - LoadsA::kVecs;
+        b.issue(l, stage + mine + 3 * kPlaneA + q * kPlaneB, q * size_b);
+        if (q == 2) b.advance(l, step_b);
+      }
+    };
+    const auto after = [&](uint32_t stage) {
+      return stage == ring + (kRing - 1) * kStage ? ring : stage + kStage;
+    };
+    i16x8 fa[2][FM][3], fb[2][FN][3];
+    const auto read = [&](int set, int r, uint32_t stage) {  // fragment r: b's, then a's
+      const int q = r % 3, f = r / 3;
+      if (f < FN) fb[set][f][q] = at_b.read(stage + 3 * kPlaneA + q * kPlaneB, delta_b(f));
+      else fa[set][f - FN][q] = at_a.read(stage + q * kPlaneA, (f - FN) * 16);
+    };
+    constexpr int kReads = 3 * (FM + FN);
+#pragma unroll
+    for (int s = 0; s < kRing; ++s)
+#pragma unroll
+      for (int l = 0; l < kLoads; ++l) issue(l, ring + s * kStage);
+    stage_landed<(kRing - 1) * kLoads>();
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read(0, r, ring);
+    constexpr int kSix[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
+    // At a step, its fragments are read by every wave, the next stage has landed, and
+    // its own place takes the stage after the ring's last.  Loads and the next
+    // fragments' reads go between the matrix instructions.
+    const auto step = [&](auto set, uint32_t now) {
+      constexpr int cur = decltype(set)::value;
+      stage_landed<(kRing - 2) * kLoads>();
+      const uint32_t next = after(now);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int h = 0; h < 3; ++h) {
+          const int g = i * 3 + h;  // of 12 groups of four matrix instructions
+#pragma unroll
+          for (int r = 2 * g; r < 2 * g + 2; ++r)
+            if (r < kReads) read(cur ^ 1, r, next);
+          if (g < kLoads) issue(g, now);
+#pragma unroll
+          for (int s = 2 * h; s < 2 * h + 2; ++s)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+              acc[i][j] = mfma_16x16x32<bf16_t>(fb[cur][j][kSix[s][0]], fa[cur][i][kSix[s][1]],
+                                                acc[i][j]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      return next;
+    };
+    static_assert(kReads <= 24 && kLoads <= 12, "all of them inside a step");
+    uint32_t now = ring;
+    for (int32_t t = 0; t < stages; t += 2) {
+      now = step(std::integral_constant<int, 0>{}, now);
+      if (t + 1 == stages) break;
+      now = step(std::integral_constant<int, 1>{}, now);
+    }
+    // no load into LDS may outlive the block
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+};
+
+// As k_ffn_rows, from planes: A [rows, K], B the expert's weights.
+template <bool B_KC, class Epilogue, int OM>
+__global__ __launch_bounds__(OM * 4) void k_ffn_rows_planes(
+    const Groups groups, const Planes A, const Planes B, int64_t N, int64_t b_rows,
+    uint32_t col_tiles, const Epilogue epilogue) {
+  typedef PlaneProduct<true, B_KC, OM> Product;
+  constexpr int FM = Product::FM, FN = Product::FN;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[Product::kRing * Product::kStage / 2];
+  constexpr int kCols = Epilogue::kDual ? kTileO / 2 : kTileO;
+  RowTile t;
+  if (!find_row_tile(groups, OM, col_tiles, block_index(), t)) return;
+  const int64_t m0 = (int64_t)t.rt * OM, n0 = (int64_t)t.ct * kCols, K = A.ld;
+  const int64_t first = t.first, last = t.count - 1 - m0, last_n = N - 1 - n0;
+  typename Product::LoadsA a;
+  a.init_kc(A.p + (first + m0) * A.ld, K,
+            [&](uint32_t i) { return (int64_t)(i < last ? i : last) * A.ld; });
+  const bf16_t* be = B.p + t.expert * b_rows * B.ld;
+  typename Product::LoadsB b;
+  if constexpr (B_KC)
+    b.init_kc(be + n0 * B.ld, K, [&](uint32_t i) {
+      const uint32_t j = i % kCols;
+      return ((int64_t)(j < last_n ? j : last_n) + (i / kCols) * N) * B.ld;
+    });
+  else
+    b.init_oc(be, B.ld, n0, B.ld, b_rows);
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  const uint32_t wm = wave % Product::WM * 64;
+  const uint32_t wn = wave / Product::WM * (kCols / Product::WN);
+  f32x4 acc[FM][FN];
+  Product::run(a, b, kWideK * 2, B_KC ? kWideK * 2 : kWideK * 2 * B.ld, A.size * 2, B.size * 2,
+               (int32_t)((K + kWideK - 1) / kWideK), Fragments<true, OM>(wm, lane),
+               Fragments<B_KC, kTileO>(wn, lane),
+               [](int j) {
+                 return Epilogue::kDual
+                            ? (uint32_t)(j % (FN / 2) * 16 + j / (FN / 2) * kCols)
+                            : (uint32_t)(j * 16);
+               },
+               lds, acc);
+  constexpr int kOut = Epilogue::kDual ? FN / 2 : FN;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = m0 + wm + i * 16 + (lane & 15u);
+    if (m >= t.count) continue;
+    typename Epilogue::Held held[kOut];
+#pragma unroll
+    for (int j = 0; j < kOut; ++j) {
+      const int64_t n = n0 + wn + j * 16 + (lane >> 4) * 4;
+      held[j] = epilogue.held(first + m, n < N ? n : N - 1);
+    }
+#pragma unroll
+    for (int j = 0; j < kOut; ++j) {
+      const int64_t n = n0 + wn + j * 16 + (lane >> 4) * 4;
+      if (n >= epilogue.columns()) continue;
+      if constexpr (Epilogue::kDual)
+        epilogue(first + m, n, acc[i][j], acc[i][j + FN / 2], held[j]);
+      else
+        epilogue(first + m, n, acc[i][j], held[j]);
+    }
+  }
+}
+
+// As k_ffn_weights, from planes.
+struct WeightPlanes {
+  Planes A[2], B[2];
+};
+template <class Out, int OM>
+__global__ __launch_bounds__(OM * 4) void k_ffn_weights_planes(
+    const WeightProducts<float> w, const WeightPlanes planes, const WeightEpilogue<Out> out) {
+  typedef PlaneProduct<false, false, OM> Product;
+  constexpr int FM = Product::FM, FN = Product::FN;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[Product::kRing * Product::kStage / 2];
+  WeightTile t;
+  if (!find_weight_tile(w, block_index(), t)) return;
+  const Group g = group_of(w.groups, t.expert);
+  int64_t from, K;
+  part_rows(g, w.parts, t.part, kWideK, from, K);
+  const int64_t M = w.M[t.product], N = w.N[t.product];
+  const int64_t m0 = (int64_t)t.rt * OM, n0 = (int64_t)t.ct * kTileO;
+  const Planes A = t.product ? planes.A[1] : planes.A[0];
+  const Planes B = t.product ? planes.B[1] : planes.B[0];
+  typename Product::LoadsA a;
+  typename Product::LoadsB b;
+  a.init_oc(A.p + (g.first + from) * A.ld, A.ld, m0, A.ld, K);
+  b.init_oc(B.p + (g.first + from) * B.ld, B.ld, n0, B.ld, K);
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  const uint32_t wm = wave % Product::WM * 64;
+  const uint32_t wn = wave / Product::WM * (kTileO / Product::WN);
+  f32x4 acc[FM][FN];
+  Product::run(a, b, kWideK * 2 * A.ld, kWideK * 2 * B.ld, A.size * 2, B.size * 2,
+               (int32_t)((K + kWideK - 1) / kWideK), Fragments<false, OM>(wm, lane),
+               Fragments<false, kTileO>(wn, lane), [](int j) { return (uint32_t)(j * 16); }, lds,
+               acc);
+  const int64_t matrix = (int64_t)t.expert * w.parts + t.part;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = m0 + wm + i * 16 + (lane & 15u);
+    if (m >= M) continue;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int64_t n = n0 + wn + j * 16 + (lane >> 4) * 4;
+      if (n < N) out(t.product, matrix, M, N, m, n, acc[i][j]);
+    }
+  }
+}
+
+}  // namespace embtab

@@ -19,9 +19,9 @@ __device__ const uint32_t kZeroVector[4] = {0u, 0u, 0u, 0u};
 // stage.  The place of a vector in LDS is the thread's own (the hardware puts a
 // wave's 64 vectors one after another), so the turning that keeps the reads free
 // of bank conflicts is in the address read from.
-template <bool KC, int THREADS>
+template <bool KC, int O, int THREADS>
 struct StageLoads {
-  static constexpr int kVecs = kWideValues / 8 / THREADS;
+  static constexpr int kVecs = O * kWideK / 8 / THREADS;
   const char* p[kVecs];
   int32_t left[kVecs];  // k values (KC) or rows (OC) from the vector's first on
 
@@ -41,30 +41,46 @@ struct StageLoads {
                                  int64_t K) {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const uint32_t v = threadIdx.x + i * THREADS, k = v >> 5;
-      const uint32_t c = (v & 31u) ^ oc_turn(k);
+      const uint32_t v = threadIdx.x + i * THREADS, k = v / (O / 8);
+      const uint32_t c = v % (O / 8) ^ oc_turn(k);
       const int64_t o = o0 + c * 8;
       p[i] = reinterpret_cast<const char*>(base + (int64_t)k * ld + (o < limit ? o : 0));
       left[i] = o < limit ? (int32_t)K - (int32_t)k : 0;
     }
   }
-  // Vector i of the next stage, to the wave's place `lds` (a byte address).  In
-  // assembly, which the compiler does not wait for: it would have every load
-  // land before each read of LDS.  No register is written.
-  __device__ inline void issue(int i, uint32_t lds, int64_t step) {
-    const char* q = left[i] > 0 ? p[i] : reinterpret_cast<const char*>(kZeroVector);
+  // Vector i of the next stage, `offset` bytes on, to the wave's place `lds` (a byte
+  // address).  In assembly, which the compiler does not wait for: it would have
+  // every load land before each read of LDS.  No register is written.
+  __device__ inline void issue(int i, uint32_t lds, int64_t offset = 0) const {
+    const char* q = left[i] > 0 ? p[i] + offset : reinterpret_cast<const char*>(kZeroVector);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
                      lds + i * THREADS * 16),
                  "v"(q)
                  : "m0");
+  }
+  // step: bytes from one stage to the next
+  __device__ inline void advance(int i, int64_t step) {
     p[i] += step;
     left[i] -= kWideK;
   }
 };
 
+// All but the last LEFT loads of every wave have landed, and every wave has its
+// fragments: what they were read from may be written.
+template <int LEFT>
+__device__ inline void stage_landed() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
+
+__device__ inline uint32_t lds_address(const void* p) {
+  typedef __attribute__((address_space(3))) const void lds_void;
+  return (uint32_t)(uintptr_t)(lds_void*)p;
+}
+
 // A lane's fragments: 16 indexes from o0 + delta on, with delta a multiple of 16
 // in the bits below o0's.  Bytes from the operand's stage on.
-template <bool KC>
+template <bool KC, int O>
 struct Fragments {
   uint32_t base, turn;
   __device__ inline Fragments(uint32_t o0, uint32_t lane) {
@@ -74,7 +90,7 @@ struct Fragments {
       turn = 0;
     } else {
       const uint32_t k = q * 8 + (i >> 2);
-      base = k * kWideO * 2 + (i & 3u) * 8;
+      base = k * O * 2 + (i & 3u) * 8;
       turn = (o0 * 2) ^ (oc_turn(k) << 4);
     }
   }
@@ -85,7 +101,7 @@ struct Fragments {
     const uint32_t at = (turn ^ (delta * 2)) + (base + stage);
     const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(uintptr_t)at);
     const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_i16x4*)(uintptr_t)(at + 4 * kWideO * 2));
+        (lds_i16x4*)(uintptr_t)(at + 4 * O * 2));
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   }
 };
@@ -94,37 +110,32 @@ template <class T, bool A_KC, bool B_KC, int WM, int WN>
 struct WideProduct {
   static constexpr int kThreads = 64 * WM * WN;
   static constexpr int FM = kWideO / WM / 16, FN = kWideO / WN / 16;
-  typedef StageLoads<A_KC, kThreads> LoadsA;
-  typedef StageLoads<B_KC, kThreads> LoadsB;
+  typedef StageLoads<A_KC, kWideO, kThreads> LoadsA;
+  typedef StageLoads<B_KC, kWideO, kThreads> LoadsB;
   static constexpr int kLoads = LoadsA::kVecs + LoadsB::kVecs;
-
-  // All but the last LEFT loads of every wave have landed, and every wave has its
-  // fragments: what they were read from may be written.
-  template <int LEFT>
-  __device__ static inline void landed() {
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LEFT) : "memory");
-  }
 
   // acc[fm][fn]; delta_b(fn): of the wave's fragment fn
   template <class Delta>
   __device__ static inline void run(LoadsA& a, LoadsB& b, int64_t step_a, int64_t step_b,
-                                    int32_t stages, const Fragments<A_KC>& at_a,
-                                    const Fragments<B_KC>& at_b, Delta delta_b, uint16_t* lds,
+                                    int32_t stages, const Fragments<A_KC, kWideO>& at_a,
+                                    const Fragments<B_KC, kWideO>& at_b, Delta delta_b, uint16_t* lds,
                                     f32x4 (&acc)[FM][FN]) {
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (stages <= 0) return;
-    typedef __attribute__((address_space(3))) uint16_t lds_value;
     constexpr uint32_t kStage = kStageValues * 2, kOperand = kWideValues * 2;
-    const uint32_t ring =
-        (uint32_t)(uintptr_t)(lds_value*)(__attribute__((address_space(3))) void*)lds;
+    const uint32_t ring = lds_address(lds);
     const uint32_t mine = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
     const auto issue = [&](int load, uint32_t stage) {
-      if (load < LoadsA::kVecs) a.issue(load, stage + mine, step_a);
-      else b.issue(load - LoadsA::kVecs, stage + mine + kOperand, step_b);
+      if (load < LoadsA::kVecs) {
+        a.issue(load, stage + mine);
+        a.advance(load, step_a);
+      } else {
+        b.issue(load - LoadsA::kVecs, stage + mine + kOperand);
+        b.advance(load - LoadsA::kVecs, step_b);
+      }
     };
     const auto after = [&](uint32_t stage) {
       return stage == ring + (kRing - 1) * kStage ? ring : stage + kStage;
@@ -134,7 +145,7 @@ struct WideProduct {
     for (int s = 0; s < kRing - 1; ++s)
 #pragma unroll
       for (int l = 0; l < kLoads; ++l) issue(l, ring + s * kStage);
-    landed<(kRing - 2) * kLoads>();
+    stage_landed<(kRing - 2) * kLoads>();
 #pragma unroll
     for (int j = 0; j < FN; ++j) fb[0][j] = at_b.read(ring + kOperand, delta_b(j));
 #pragma unroll
@@ -163,7 +174,7 @@ struct WideProduct {
     // the places of t - 1 and t.
     uint32_t now = ring;
     for (int32_t t = 0; t < stages; t += 2) {
-      landed<kLoads>();
+      stage_landed<kLoads>();
       const uint32_t next = after(now), second = after(next);
       const uint32_t before = now == ring ? ring + (kRing - 1) * kStage : now - kStage;
       step(std::integral_constant<int, 0>{}, next, before);
@@ -202,8 +213,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ffn_rows_wide(
     b.init_oc(be, N, n0, N, K);
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
   const uint32_t wm = wave % WM * (kWideO / WM), wn = wave / WM * (kCols / WN);
-  const Fragments<true> at_a(wm, lane);
-  const Fragments<B_KC> at_b(wn, lane);
+  const Fragments<true, kWideO> at_a(wm, lane);
+  const Fragments<B_KC, kWideO> at_b(wn, lane);
   f32x4 acc[FM][FN];
   Product::run(a, b, kWideK * 2, B_KC ? kWideK * 2 : (int64_t)kWideK * 2 * N,
                (int32_t)((K + kWideK - 1) / kWideK), at_a, at_b,
@@ -264,8 +275,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ffn_weights_wide(
   const uint32_t wm = wave % WM * (kWideO / WM), wn = wave / WM * (kWideO / WN);
   f32x4 acc[FM][FN];
   Product::run(a, b, (int64_t)kWideK * 2 * M, (int64_t)kWideK * 2 * N,
-               (int32_t)((K + kWideK - 1) / kWideK), Fragments<false>(wm, lane),
-               Fragments<false>(wn, lane), [](int j) { return (uint32_t)(j * 16); }, lds, acc);
+               (int32_t)((K + kWideK - 1) / kWideK), Fragments<false, kWideO>(wm, lane),
+               Fragments<false, kWideO>(wn, lane), [](int j) { return (uint32_t)(j * 16); }, lds, acc);
   const int64_t matrix = (int64_t)t.expert * w.parts + t.part;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
