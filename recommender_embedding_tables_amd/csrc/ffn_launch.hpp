@@ -60,6 +60,10 @@ __global__ __launch_bounds__(256) void k_ffn_add_parts(const float* __restrict__
   store4(out + e * size + i, t, size - i);
 }
 
+// The 256 x 256 tiles hold offsets of 32 bits: those of 256 rows, of 64 rows of the
+// other operand, or of a projection behind the other.
+bool wide_offsets(int64_t K, int64_t N) { return K * N < (1ll << 30) && K + N < (1ll << 20); }
+
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 #ifndef FEW
@@ -88,7 +92,7 @@ hipError_t rows_product(const Groups& g, const void* a, const void* b, int64_t K
       return few_rows_product<T>(g, a, b, K, N, b_stride, epilogue, s);
   }
   if constexpr (sizeof(T) == 2) {
-    if (K % 8 == 0 && (B_KC || N % 8 == 0) && on16(a) && on16(b)) {
+    if (K % 8 == 0 && (B_KC || N % 8 == 0) && on16(a) && on16(b) && wide_offsets(K, N)) {
       constexpr int WM = 2, WN = 4;
       const int64_t cols = Epilogue::kDual ? kWideO / 2 : kWideO;
       const int64_t col_tiles = (N + cols - 1) / cols;

@@ -140,6 +140,78 @@ struct StorePlanesEpilogue : StoreEpilogue<float> {
 };
 
 // ---------------------------------------------------------------- product
+template <bool KC, int O, int THREADS>
+struct StageLoads {
+  static constexpr int kVecs = O * kHalfK / 8 / THREADS;
+  const char* p[kVecs];
+  int32_t left[kVecs];  // k values (KC) or rows (OC) from the vector's first on
+
+  // row(i): offset in values of the operand's index i (KC)
+  template <class T, class Row>
+  __device__ inline void init_kc(const T* base, int64_t K, Row row) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const uint32_t v = threadIdx.x + i * THREADS, r = v >> 2;
+      const uint32_t c = (v & 3u) ^ kc_turn(r);
+      p[i] = reinterpret_cast<const char*>(base + row(r) + c * 8);
+      left[i] = (int32_t)K - (int32_t)(c * 8);
+    }
+  }
+  template <class T>
+  __device__ inline void init_oc(const T* base, int64_t ld, int64_t o0, int64_t limit,
+                                 int64_t K) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const uint32_t v = threadIdx.x + i * THREADS, k = v / (O / 8);
+      const uint32_t c = v % (O / 8) ^ oc_turn(k);
+      const int64_t o = o0 + c * 8;
+      p[i] = reinterpret_cast<const char*>(base + (int64_t)k * ld + (o < limit ? o : 0));
+      left[i] = o < limit ? (int32_t)K - (int32_t)k : 0;
+    }
+  }
+  // Vector i of the next stage, `offset` bytes on, to the wave's place `lds` (a byte
+  // address).  In assembly, which the compiler does not wait for: it would have
+  // every load land before each read of LDS.  No register is written.
+  __device__ inline void issue(int i, uint32_t lds, int64_t offset = 0) const {
+    const char* q = left[i] > 0 ? p[i] + offset : reinterpret_cast<const char*>(kZeroVector);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
+                     lds + i * THREADS * 16),
+                 "v"(q)
+                 : "m0");
+  }
+  // step: bytes from one stage to the next
+  __device__ inline void advance(int i, int64_t step) {
+    p[i] += step;
+    left[i] -= kHalfK;
+  }
+};
+
+template <bool KC, int O>
+struct Fragments {
+  uint32_t base, turn;
+  __device__ inline Fragments(uint32_t o0, uint32_t lane) {
+    const uint32_t i = lane & 15u, q = lane >> 4;
+    if (KC) {
+      base = ((o0 + i) * kHalfK + ((q ^ kc_turn(i)) << 3)) * 2;
+      turn = 0;
+    } else {
+      const uint32_t k = q * 8 + (i >> 2);
+      base = k * O * 2 + (i & 3u) * 8;
+      turn = (o0 * 2) ^ (oc_turn(k) << 4);
+    }
+  }
+  __device__ inline i16x8 read(uint32_t stage, uint32_t delta) const {
+    typedef __attribute__((address_space(3))) i16x8 lds_i16x8;
+    typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+    if (KC) return *(const lds_i16x8*)(uintptr_t)(base + stage + delta * (kHalfK * 2));
+    const uint32_t at = (turn ^ (delta * 2)) + (base + stage);
+    const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(uintptr_t)at);
+    const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_i16x4*)(uintptr_t)(at + 4 * O * 2));
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+
 // Tiles of OM x 128 by waves of 64 x 32: 128 rows by eight waves and a ring of
 // three stages, 64 rows by four and a ring of four (144 KB of LDS either way).  A
 // stage holds 32 k of both operands' planes.
@@ -150,7 +222,7 @@ struct PlaneProduct {
   typedef StageLoads<A_KC, OM, kThreads> LoadsA;
   typedef StageLoads<B_KC, kTileO, kThreads> LoadsB;
   static constexpr int kLoads = 3 * (LoadsA::kVecs + LoadsB::kVecs);
-  static constexpr uint32_t kPlaneA = OM * kWideK * 2, kPlaneB = kTileO * kWideK * 2;
+  static constexpr uint32_t kPlaneA = OM * kHalfK * 2, kPlaneB = kTileO * kHalfK * 2;
   static constexpr uint32_t kStage = 3 * (kPlaneA + kPlaneB);
 
   // size_a, size_b: bytes of a plane
@@ -263,8 +335,8 @@ __global__ __launch_bounds__(OM * 4) void k_ffn_rows_planes(
   const uint32_t wm = wave % Product::WM * 64;
   const uint32_t wn = wave / Product::WM * (kCols / Product::WN);
   f32x4 acc[FM][FN];
-  Product::run(a, b, kWideK * 2, B_KC ? kWideK * 2 : kWideK * 2 * B.ld, A.size * 2, B.size * 2,
-               (int32_t)((K + kWideK - 1) / kWideK), Fragments<true, OM>(wm, lane),
+  Product::run(a, b, kHalfK * 2, B_KC ? kHalfK * 2 : kHalfK * 2 * B.ld, A.size * 2, B.size * 2,
+               (int32_t)((K + kHalfK - 1) / kHalfK), Fragments<true, OM>(wm, lane),
                Fragments<B_KC, kTileO>(wn, lane),
                [](int j) {
                  return Epilogue::kDual
@@ -309,7 +381,7 @@ __global__ __launch_bounds__(OM * 4) void k_ffn_weights_planes(
   if (!find_weight_tile(w, block_index(), t)) return;
   const Group g = group_of(w.groups, t.expert);
   int64_t from, K;
-  part_rows(g, w.parts, t.part, kWideK, from, K);
+  part_rows(g, w.parts, t.part, kHalfK, from, K);
   const int64_t M = w.M[t.product], N = w.N[t.product];
   const int64_t m0 = (int64_t)t.rt * OM, n0 = (int64_t)t.ct * kTileO;
   const Planes A = t.product ? planes.A[1] : planes.A[0];
@@ -322,8 +394,8 @@ __global__ __launch_bounds__(OM * 4) void k_ffn_weights_planes(
   const uint32_t wm = wave % Product::WM * 64;
   const uint32_t wn = wave / Product::WM * (kTileO / Product::WN);
   f32x4 acc[FM][FN];
-  Product::run(a, b, kWideK * 2 * A.ld, kWideK * 2 * B.ld, A.size * 2, B.size * 2,
-               (int32_t)((K + kWideK - 1) / kWideK), Fragments<false, OM>(wm, lane),
+  Product::run(a, b, kHalfK * 2 * A.ld, kHalfK * 2 * B.ld, A.size * 2, B.size * 2,
+               (int32_t)((K + kHalfK - 1) / kHalfK), Fragments<false, OM>(wm, lane),
                Fragments<false, kTileO>(wn, lane), [](int j) { return (uint32_t)(j * 16); }, lds,
                acc);
   const int64_t matrix = (int64_t)t.expert * w.parts + t.part;

@@ -1,4 +1,16 @@
 // Grouped matrix products of 16-bit values in tiles of 256 x 256, for gfx950.
+//
+// Bound by the matrix instructions, which keep the card at its power limit, and by
+// the way from L2 into LDS (10 TB/s in these kernels): the largest tile that eight
+// waves hold in registers (128 x 64 results each) moves the fewest bytes, and both
+// operands go from memory straight into LDS, in lines of 128 bytes.  (In stages of
+// 32 k, with 64 bytes of a row at a time, L2 serves twice the requests for the same
+// bytes: 32768 x 3328 x 3328, both with k innermost, 748 us against @.)
+//
+// LDS holds two slots of 64 k.  Each half slot is a step of 32 matrix instructions
+// a wave; the next step's fragments are read into a second set of registers between
+// them.  One barrier a slot, between its halves: by then every wave has read the
+// slot out and the other has landed, so the slot after the next is sent for.
 #pragma once
 
 #include <utility>
@@ -7,63 +19,39 @@
 
 namespace embtab {
 
-constexpr int kWideO = 256, kWideK = 32;
-constexpr int kRing = 5;                              // stages of LDS
-constexpr int kWideValues = kWideO * kWideK;          // of one operand's stage
-constexpr int kStageValues = 2 * kWideValues;
+constexpr int kWideO = 256, kWideK = 64, kHalfK = 32;
+constexpr int kWideValues = kWideO * kWideK;  // of one operand's slot
+constexpr int kSlotValues = 2 * kWideValues;
 
 // Sixteen bytes of zeros that vectors past the end are taken from.
 __device__ const uint32_t kZeroVector[4] = {0u, 0u, 0u, 0u};
 
-// Loads of one operand straight into LDS: THREADS threads, kVecs vectors each a
-// stage.  The place of a vector in LDS is the thread's own (the hardware puts a
-// wave's 64 vectors one after another), so the turning that keeps the reads free
-// of bank conflicts is in the address read from.
-template <bool KC, int O, int THREADS>
-struct StageLoads {
-  static constexpr int kVecs = O * kWideK / 8 / THREADS;
-  const char* p[kVecs];
-  int32_t left[kVecs];  // k values (KC) or rows (OC) from the vector's first on
+__device__ inline uint32_t lds_address(const void* p) {
+  typedef __attribute__((address_space(3))) const void lds_void;
+  return (uint32_t)(uintptr_t)(lds_void*)p;
+}
 
-  // row(i): offset in values of the operand's index i (KC)
-  template <class T, class Row>
-  __device__ inline void init_kc(const T* base, int64_t K, Row row) {
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const uint32_t v = threadIdx.x + i * THREADS, r = v >> 2;
-      const uint32_t c = (v & 3u) ^ kc_turn(r);
-      p[i] = reinterpret_cast<const char*>(base + row(r) + c * 8);
-      left[i] = (int32_t)K - (int32_t)(c * 8);
-    }
-  }
-  template <class T>
-  __device__ inline void init_oc(const T* base, int64_t ld, int64_t o0, int64_t limit,
-                                 int64_t K) {
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const uint32_t v = threadIdx.x + i * THREADS, k = v / (O / 8);
-      const uint32_t c = v % (O / 8) ^ oc_turn(k);
-      const int64_t o = o0 + c * 8;
-      p[i] = reinterpret_cast<const char*>(base + (int64_t)k * ld + (o < limit ? o : 0));
-      left[i] = o < limit ? (int32_t)K - (int32_t)k : 0;
-    }
-  }
-  // Vector i of the next stage, `offset` bytes on, to the wave's place `lds` (a byte
-  // address).  In assembly, which the compiler does not wait for: it would have
-  // every load land before each read of LDS.  No register is written.
-  __device__ inline void issue(int i, uint32_t lds, int64_t offset = 0) const {
-    const char* q = left[i] > 0 ? p[i] + offset : reinterpret_cast<const char*>(kZeroVector);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
-                     lds + i * THREADS * 16),
-                 "v"(q)
-                 : "m0");
-  }
-  // step: bytes from one stage to the next
-  __device__ inline void advance(int i, int64_t step) {
-    p[i] += step;
-    left[i] -= kWideK;
-  }
-};
+// A vector of 16 bytes to each lane's place behind the wave's `lds` (a byte
+// address), from a lane's address or from a lane's offset behind a common one.  In
+// assembly, which the compiler does not wait for: it would have every load land
+// before each read of LDS.  No register is written.
+__device__ inline void load_to_lds(const char* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds),
+               "v"(p)
+               : "m0");
+}
+__device__ inline void load_to_lds(const char* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds),
+               "v"(offset), "s"(base)
+               : "m0");
+}
+template <class P>
+__device__ inline const P* common_pointer(const P* p) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return reinterpret_cast<const P*>((uintptr_t)(((uint64_t)hi << 32) | lo));
+}
 
 // All but the last LEFT loads of every wave have landed, and every wave has its
 // fragments: what they were read from may be written.
@@ -73,35 +61,97 @@ __device__ inline void stage_landed() {
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
 
-__device__ inline uint32_t lds_address(const void* p) {
-  typedef __attribute__((address_space(3))) const void lds_void;
-  return (uint32_t)(uintptr_t)(lds_void*)p;
-}
+// The eight 16-byte pieces of a KC row of 128 bytes are turned by the row, so that
+// the 16 lanes a read serves at once (ffn_tiles.hpp) meet no bank twice.
+__device__ inline uint32_t wide_kc_turn(uint32_t row) { return (row >> 1) & 7u; }
+
+// Loads of one operand straight into LDS: THREADS threads, kVecs vectors each a
+// slot.  The place of a vector in LDS is the thread's own (the hardware puts a
+// wave's 64 vectors one after another), so the turning is in the address read from;
+// it is the same for all of a thread's vectors.
+template <bool KC, int THREADS>
+struct WideLoads {
+  static constexpr int kVecs = kWideValues / 8 / THREADS;
+  static constexpr int kRows = THREADS / (KC ? 8 : kWideO / 8);  // from a vector to the next
+  const char* base;        // of the next slot, the same in every lane
+  uint32_t offset[kVecs];  // bytes from there
+  int64_t left;            // k values from the slot on
+
+  // k of the thread's first vector in a slot; formed where it is needed, a register
+  // less in the loop
+  static __device__ inline uint32_t first_k() {
+    uint32_t t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return KC ? ((t & 7u) ^ wide_kc_turn(t >> 3)) * 8 : t / (kWideO / 8);
+  }
+
+  // row(i): offset in values of the operand's index i, below 2^31 (KC)
+  template <class T, class Row>
+  __device__ inline void init_kc(const T* p, int64_t K, Row row) {
+    base = reinterpret_cast<const char*>(common_pointer(p));
+    left = K;
+    const uint32_t k = first_k();
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      offset[i] = (uint32_t)(row((threadIdx.x >> 3) + i * kRows) + k) * 2;
+  }
+  // columns o0 on of `limit`, rows of ld values; one past the end takes the first
+  template <class T>
+  __device__ inline void init_oc(const T* p, int64_t ld, int64_t o0, int64_t limit, int64_t K) {
+    base = reinterpret_cast<const char*>(common_pointer(p + o0));
+    left = K;
+    const uint32_t k = first_k();
+    const uint32_t c = (threadIdx.x % (kWideO / 8) ^ oc_turn(k)) * 8;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      offset[i] = (uint32_t)((k + i * kRows) * ld + (o0 + c < limit ? c : 0)) * 2;
+  }
+  // Vector i of the next slot.  A slot past the end is not loaded, a vector past it
+  // is zeros.
+  __device__ inline void issue(int i, uint32_t lds) const {
+    const uint32_t to = lds + i * THREADS * 16;
+    if (left >= kWideK) {
+      load_to_lds(base, offset[i], to);
+    } else if (left > 0) {
+      const int64_t k = first_k() + (KC ? 0 : i * kRows);
+      load_to_lds(k < left ? base + offset[i] : reinterpret_cast<const char*>(kZeroVector), to);
+    }
+  }
+  // step: bytes from one slot to the next
+  __device__ inline void advance(int64_t step) {
+    base += step;
+    left -= kWideK;
+  }
+};
 
 // A lane's fragments: 16 indexes from o0 + delta on, with delta a multiple of 16
-// in the bits below o0's.  Bytes from the operand's stage on.
-template <bool KC, int O>
-struct Fragments {
-  uint32_t base, turn;
-  __device__ inline Fragments(uint32_t o0, uint32_t lane) {
+// in the bits below o0's, and half 0 or 1 of a slot's k.  Bytes from the operand's
+// slot on.
+template <bool KC>
+struct WideFragments {
+  uint32_t base[2], turn;
+  __device__ inline WideFragments(uint32_t o0, uint32_t lane) {
     const uint32_t i = lane & 15u, q = lane >> 4;
     if (KC) {
-      base = ((o0 + i) * kWideK + ((q ^ kc_turn(i)) << 3)) * 2;
+#pragma unroll
+      for (uint32_t h = 0; h < 2; ++h)
+        base[h] = (o0 + i) * (kWideK * 2) + (((h * 4 + q) ^ wide_kc_turn(i)) << 4);
       turn = 0;
     } else {
       const uint32_t k = q * 8 + (i >> 2);
-      base = k * O * 2 + (i & 3u) * 8;
+      base[0] = k * kWideO * 2 + (i & 3u) * 8;
+      base[1] = base[0] + kHalfK * kWideO * 2;
       turn = (o0 * 2) ^ (oc_turn(k) << 4);
     }
   }
-  __device__ inline i16x8 read(uint32_t stage, uint32_t delta) const {
+  __device__ inline i16x8 read(uint32_t slot, int half, uint32_t delta) const {
     typedef __attribute__((address_space(3))) i16x8 lds_i16x8;
     typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-    if (KC) return *(const lds_i16x8*)(uintptr_t)(base + stage + delta * (kWideK * 2));
-    const uint32_t at = (turn ^ (delta * 2)) + (base + stage);
+    if (KC) return *(const lds_i16x8*)(uintptr_t)(base[half] + slot + delta * (kWideK * 2));
+    const uint32_t at = (turn ^ (delta * 2)) + (base[half] + slot);
     const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(uintptr_t)at);
     const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_i16x4*)(uintptr_t)(at + 4 * O * 2));
+        (lds_i16x4*)(uintptr_t)(at + 4 * kWideO * 2));
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   }
 };
@@ -110,77 +160,77 @@ template <class T, bool A_KC, bool B_KC, int WM, int WN>
 struct WideProduct {
   static constexpr int kThreads = 64 * WM * WN;
   static constexpr int FM = kWideO / WM / 16, FN = kWideO / WN / 16;
-  typedef StageLoads<A_KC, kWideO, kThreads> LoadsA;
-  typedef StageLoads<B_KC, kWideO, kThreads> LoadsB;
+  typedef WideLoads<A_KC, kThreads> LoadsA;
+  typedef WideLoads<B_KC, kThreads> LoadsB;
   static constexpr int kLoads = LoadsA::kVecs + LoadsB::kVecs;
 
-  // acc[fm][fn]; delta_b(fn): of the wave's fragment fn
+  // acc[fm][fn] over K; step_a, step_b: bytes from one slot to the next;
+  // delta_b(fn): of the wave's fragment fn
   template <class Delta>
   __device__ static inline void run(LoadsA& a, LoadsB& b, int64_t step_a, int64_t step_b,
-                                    int32_t stages, const Fragments<A_KC, kWideO>& at_a,
-                                    const Fragments<B_KC, kWideO>& at_b, Delta delta_b, uint16_t* lds,
-                                    f32x4 (&acc)[FM][FN]) {
+                                    int64_t K, const WideFragments<A_KC>& at_a,
+                                    const WideFragments<B_KC>& at_b, Delta delta_b,
+                                    uint16_t* lds, f32x4 (&acc)[FM][FN]) {
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (stages <= 0) return;
-    constexpr uint32_t kStage = kStageValues * 2, kOperand = kWideValues * 2;
-    const uint32_t ring = lds_address(lds);
+    const int32_t steps = (int32_t)((K + kHalfK - 1) / kHalfK);
+    if (steps <= 0) return;
+    constexpr uint32_t kSlot = kSlotValues * 2, kOperand = kWideValues * 2;
+    const uint32_t first = lds_address(lds);
     const uint32_t mine = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
-    const auto issue = [&](int load, uint32_t stage) {
-      if (load < LoadsA::kVecs) {
-        a.issue(load, stage + mine);
-        a.advance(load, step_a);
-      } else {
-        b.issue(load - LoadsA::kVecs, stage + mine + kOperand);
-        b.advance(load - LoadsA::kVecs, step_b);
-      }
+    const auto issue = [&](int load, uint32_t slot) {
+      if (load < LoadsA::kVecs) a.issue(load, slot + mine);
+      else b.issue(load - LoadsA::kVecs, slot + mine + kOperand);
     };
-    const auto after = [&](uint32_t stage) {
-      return stage == ring + (kRing - 1) * kStage ? ring : stage + kStage;
+    const auto advance = [&] {
+      a.advance(step_a);
+      b.advance(step_b);
     };
     i16x8 fa[2][FM], fb[2][FN];
 #pragma unroll
-    for (int s = 0; s < kRing - 1; ++s)
+    for (int s = 0; s < 2; ++s) {
 #pragma unroll
-      for (int l = 0; l < kLoads; ++l) issue(l, ring + s * kStage);
-    stage_landed<(kRing - 2) * kLoads>();
+      for (int l = 0; l < kLoads; ++l) issue(l, first + s * kSlot);
+      advance();
+    }
+    if (steps > 2) stage_landed<kLoads>();
+    else stage_landed<0>();
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[0][j] = at_b.read(ring + kOperand, delta_b(j));
+    for (int j = 0; j < FN; ++j) fb[0][j] = at_b.read(first + kOperand, 0, delta_b(j));
 #pragma unroll
-    for (int i = 0; i < FM; ++i) fa[0][i] = at_a.read(ring, i * 16);
-    // A stage's matrix instructions, with the reads of the next stage's fragments
-    // and the loads of a later one between them.
+    for (int i = 0; i < FM; ++i) fa[0][i] = at_a.read(first, 0, i * 16);
+    // A step's matrix instructions, and between them the reads of the next step's
+    // fragments and, in a slot's second step, the loads of the slot after the next.
     constexpr int kReads = (FM + FN + FM - 3) / (FM - 2);  // a row, none in the last two
-    const auto step = [&](auto set, uint32_t next, uint32_t in) {
-      constexpr int now = decltype(set)::value;
+    const auto step = [&](auto place, uint32_t from, uint32_t in) {
+      constexpr int now = decltype(place)::value, next = now ^ 1;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
 #pragma unroll
         for (int r = i * kReads; r < (i + 1) * kReads; ++r) {
-          if (r < FN) fb[now ^ 1][r] = at_b.read(next + kOperand, delta_b(r));
-          else if (r < FN + FM) fa[now ^ 1][r - FN] = at_a.read(next, (r - FN) * 16);
+          if (r < FN) fb[next][r] = at_b.read(from + kOperand, next, delta_b(r));
+          else if (r < FN + FM) fa[next][r - FN] = at_a.read(from, next, (r - FN) * 16);
         }
-        if ((i + 1) * kLoads / FM > i * kLoads / FM) issue(i * kLoads / FM, in);
+        if (now == 1)
+#pragma unroll
+          for (int l = i * kLoads / FM; l < (i + 1) * kLoads / FM; ++l) issue(l, in);
 #pragma unroll
         for (int j = 0; j < FN; ++j)
           acc[i][j] = mfma_16x16x32<T>(fb[now][j], fa[now][i], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    // Two stages to a barrier.  At stage t's, the fragments of t are read, t + 1
-    // and t + 2 have landed, t + 3 is on its way, and t + 4 and t + 5 are sent to
-    // the places of t - 1 and t.
-    uint32_t now = ring;
-    for (int32_t t = 0; t < stages; t += 2) {
-      stage_landed<kLoads>();
-      const uint32_t next = after(now), second = after(next);
-      const uint32_t before = now == ring ? ring + (kRing - 1) * kStage : now - kStage;
-      step(std::integral_constant<int, 0>{}, next, before);
-      if (t + 1 == stages) break;
-      step(std::integral_constant<int, 1>{}, second, now);
-      now = second;
+    uint32_t slot = first;
+    for (int32_t t = 0; t < steps; t += 2) {
+      step(std::integral_constant<int, 0>{}, slot, 0u);
+      if (t + 1 == steps) break;
+      stage_landed<0>();
+      const uint32_t other = slot == first ? first + kSlot : first;
+      step(std::integral_constant<int, 1>{}, other, slot);
+      advance();
+      slot = other;
     }
     // no load into LDS may outlive the block
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -193,7 +243,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ffn_rows_wide(
     int64_t b_stride, uint32_t col_tiles, const Epilogue epilogue) {
   typedef WideProduct<T, true, B_KC, WM, WN> Product;
   constexpr int FM = Product::FM, FN = Product::FN;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[kRing * kStageValues];
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * kSlotValues];
   constexpr int kCols = Epilogue::kDual ? kWideO / 2 : kWideO;
   RowTile t;
   if (!find_row_tile(groups, kWideO, col_tiles, block_index(), t)) return;
@@ -213,11 +263,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ffn_rows_wide(
     b.init_oc(be, N, n0, N, K);
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
   const uint32_t wm = wave % WM * (kWideO / WM), wn = wave / WM * (kCols / WN);
-  const Fragments<true, kWideO> at_a(wm, lane);
-  const Fragments<B_KC, kWideO> at_b(wn, lane);
+  const WideFragments<true> at_a(wm, lane);
+  const WideFragments<B_KC> at_b(wn, lane);
   f32x4 acc[FM][FN];
   Product::run(a, b, kWideK * 2, B_KC ? kWideK * 2 : (int64_t)kWideK * 2 * N,
-               (int32_t)((K + kWideK - 1) / kWideK), at_a, at_b,
+               K, at_a, at_b,
                [](int j) {
                  return Epilogue::kDual
                             ? (uint32_t)(j % (FN / 2) * 16 + j / (FN / 2) * kCols)
@@ -259,12 +309,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ffn_weights_wide(
     const WeightProducts<T> w, const WeightEpilogue<Out> out) {
   typedef WideProduct<T, false, false, WM, WN> Product;
   constexpr int FM = Product::FM, FN = Product::FN;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[kRing * kStageValues];
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * kSlotValues];
   WeightTile t;
   if (!find_weight_tile(w, block_index(), t)) return;
   const Group g = group_of(w.groups, t.expert);
   int64_t from, K;
-  part_rows(g, w.parts, t.part, kWideK, from, K);
+  part_rows(g, w.parts, t.part, kHalfK, from, K);
   const int64_t M = w.M[t.product], N = w.N[t.product];
   const int64_t m0 = (int64_t)t.rt * kWideO, n0 = (int64_t)t.ct * kWideO;
   typename Product::LoadsA a;
@@ -275,8 +325,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ffn_weights_wide(
   const uint32_t wm = wave % WM * (kWideO / WM), wn = wave / WM * (kWideO / WN);
   f32x4 acc[FM][FN];
   Product::run(a, b, (int64_t)kWideK * 2 * M, (int64_t)kWideK * 2 * N,
-               (int32_t)((K + kWideK - 1) / kWideK), Fragments<false, kWideO>(wm, lane),
-               Fragments<false, kWideO>(wn, lane), [](int j) { return (uint32_t)(j * 16); }, lds, acc);
+               K, WideFragments<false>(wm, lane),
+               WideFragments<false>(wn, lane), [](int j) { return (uint32_t)(j * 16); }, lds, acc);
   const int64_t matrix = (int64_t)t.expert * w.parts + t.part;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
