@@ -199,12 +199,9 @@ inline dim3 tile_grid(int64_t blocks, int threads) {
 }
 
 // ---------------------------------------------------------------- activations
-// act(v) and its slope.  16-bit data takes the hardware's exponential and
-// reciprocal (within a few 2^-23, far below its own rounding).
-struct ActValue {
-  float a, slope;
-};
-
+// act(v) and its slope for N values (one choice of the activation for all).  16-bit
+// data takes the hardware's exponential and reciprocal (within a few 2^-23, far
+// below its own rounding).
 template <class T>
 __device__ inline void logistic(float v, float& s, float& rest) {  // s(v) and 1 - s(v)
   float t;
@@ -218,61 +215,83 @@ __device__ inline void logistic(float v, float& s, float& rest) {  // s(v) and 1
   rest = v > 0.0f ? t * s : 1.0f - s;  // 1 - s cancels where s is near 1
 }
 
-template <class T>
-__device__ inline ActValue act_value(int32_t act, float v) {
-  if (act == EMB_ACT_SILU) {
-    float s, rest;
-    logistic<T>(v, s, rest);
-    return {v * s, s + v * (s * rest)};
+template <class T, int N>
+__device__ inline void activate(int32_t act, const float (&v)[N], float (&a)[N],
+                                float (&slope)[N]) {
+  if (act == EMB_ACT_SILU || act == EMB_ACT_SIGMOID) {
+    const bool silu = act == EMB_ACT_SILU;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s, rest;
+      logistic<T>(v[i], s, rest);
+      a[i] = silu ? v[i] * s : s;
+      slope[i] = silu ? s + v[i] * (s * rest) : s * rest;
+    }
+  } else if (act == EMB_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float cdf = 0.5f * erfcf(v[i] * -0.70710678118654752440f);
+      a[i] = v[i] * cdf;
+      slope[i] = cdf + v[i] * (0.39894228040143267794f * expf(-0.5f * v[i] * v[i]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      a[i] = v[i] <= 0.0f ? 0.0f : v[i];
+      slope[i] = v[i] <= 0.0f ? 0.0f : 1.0f;
+    }
   }
-  if (act == EMB_ACT_GELU) {
-    const float cdf = 0.5f * erfcf(v * -0.70710678118654752440f);
-    return {v * cdf, cdf + v * (0.39894228040143267794f * expf(-0.5f * v * v))};
-  }
-  if (act == EMB_ACT_RELU) return {v <= 0.0f ? 0.0f : v, v <= 0.0f ? 0.0f : 1.0f};
-  float s, rest;
-  logistic<T>(v, s, rest);
-  return {s, s * rest};
 }
 
-// ---------------------------------------------------------------- stores
-// The first n of four neighbouring values, each rounded once.
-template <class T>
-__device__ inline void store4(T* p, f32x4 v, int64_t n) {
-  if (n >= 4) {
-    if constexpr (sizeof(T) == 4) {
-      Raw<float> r;
+// ---------------------------------------------------------------- values
+// W neighbouring values in memory, 8 or 16 bytes (or twice 16), and the first n of
+// them.
+template <class T, int W>
+struct Span {
+  static constexpr int kPer = W < kVec<T> ? W : kVec<T>;
+  Raw<T, kPer> r[W / kPer];
+  __device__ inline float get(int i) const { return r[i / kPer].get(i % kPer); }
+};
+
+template <int W, class T>
+__device__ inline void store_span(T* p, const float (&v)[W], int64_t n) {
+  typedef Span<T, W> S;
+  if (n >= W) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r.w[i] = __float_as_uint(v[i]);
-      store_raw(p, r);
-    } else {
-      Raw<T, 4> r;
-      const float f[4] = {v[0], v[1], v[2], v[3]};
-      r.set_all(f);
-      store_raw<T, 4>(p, r);
+    for (int k = 0; k < W / S::kPer; ++k) {
+      Raw<T, S::kPer> r;
+      r.set_all(v + k * S::kPer);
+      store_raw<T, S::kPer>(p + k * S::kPer, r);
     }
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < W; ++i)
     if (i < n) p[i] = from_f32<T>(v[i]);
 }
 
-// The first n of four neighbouring values, then zeros.
-template <class T>
-__device__ inline Raw<T, 4> load_part4(const T* p, int64_t n) {
-  if (n >= 4) return load_raw<T, 4>(p);
-  float f[4];
+// zeros behind the first n
+template <int W, class T>
+__device__ inline Span<T, W> load_span(const T* p, int64_t n) {
+  typedef Span<T, W> S;
+  S s;
+  if (n >= W) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = i < n ? to_f32(p[i]) : 0.0f;
-  Raw<T, 4> r;
-  r.set_all(f);
-  return r;
+    for (int k = 0; k < W / S::kPer; ++k) s.r[k] = load_raw<T, S::kPer>(p + k * S::kPer);
+    return s;
+  }
+  float f[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) f[i] = i < n ? to_f32(p[i]) : 0.0f;
+#pragma unroll
+  for (int k = 0; k < W / S::kPer; ++k) s.r[k].set_all(f + k * S::kPer);
+  return s;
 }
 
 // ---------------------------------------------------------------- epilogues
-// Of four neighbouring columns from n on, of `width`, in row `row` of the buffer.  held(): what it reads of
-// them, for callers that have these loads on their way before they are needed.
+// Of W neighbouring columns from n on, in a row of the buffer.  row(): its places;
+// held(): what is read there, for callers that have these loads on their way before
+// they are needed.
 struct NothingHeld {};
 
 template <class T>
@@ -280,20 +299,20 @@ struct StoreEpilogue {
   static constexpr bool kDual = false;
   T* out;
   int64_t width;
-  typedef NothingHeld Held;
-  __device__ inline Held held(int64_t, int64_t) const { return {}; }
-  __device__ inline void operator()(int64_t row, int64_t n, f32x4 v, Held) const {
-    store4(out + row * width + n, v, width - n);
+  struct Row {
+    T* out;
+  };
+  template <int W>
+  using Held = NothingHeld;
+  __device__ inline Row row(int64_t r) const { return {out + r * width}; }
+  template <int W>
+  __device__ inline Held<W> held(const Row&, int64_t) const {
+    return {};
   }
-};
-
-// Weight gradients: the expert's matrices, or the parts' sums, [expert][part].
-template <class Out>
-struct WeightEpilogue {
-  Out* out[2];
-  __device__ inline void operator()(int32_t product, int64_t matrix, int64_t M, int64_t N,
-                                    int64_t m, int64_t n, f32x4 v) const {
-    store4(out[product] + (matrix * M + m) * N + n, v, N - n);
+  template <int W>
+  __device__ inline void store(const Row& r, int64_t n, const float (&v)[W],
+                               const Held<W>&) const {
+    store_span(r.out + n, v, width - n);
   }
 };
 
@@ -304,22 +323,36 @@ struct ActEpilogue {
   T *gu, *a;  // gu: null where it is not kept
   int64_t width;
   int32_t act;
-  typedef NothingHeld Held;
-  __device__ inline Held held(int64_t, int64_t) const { return {}; }
-  __device__ inline f32x4 product(int64_t row, int64_t n, f32x4 g, f32x4 u) const {
-    const int64_t have = width - n;
-    if (gu) {
-      store4(gu + row * 2 * width + n, g, have);
-      store4(gu + (row * 2 + 1) * width + n, u, have);
-    }
-    f32x4 p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = act_value<T>(act, g[i]).a * u[i];
-    store4(a + row * width + n, p, have);
-    return p;
+  struct Row {
+    T *gu, *a;
+  };
+  template <int W>
+  using Held = NothingHeld;
+  __device__ inline Row row(int64_t r) const {
+    return {gu ? gu + r * 2 * width : nullptr, a + r * width};
   }
-  __device__ inline void operator()(int64_t row, int64_t n, f32x4 g, f32x4 u, Held) const {
-    product(row, n, g, u);
+  template <int W>
+  __device__ inline Held<W> held(const Row&, int64_t) const {
+    return {};
+  }
+  template <int W>
+  __device__ inline void product(const Row& r, int64_t n, const float (&g)[W],
+                                 const float (&u)[W], float (&p)[W]) const {
+    if (r.gu) {
+      store_span(r.gu + n, g, width - n);
+      store_span(r.gu + width + n, u, width - n);
+    }
+    float slope[W];
+    activate<T>(act, g, p, slope);
+#pragma unroll
+    for (int i = 0; i < W; ++i) p[i] *= u[i];
+    store_span(r.a + n, p, width - n);
+  }
+  template <int W>
+  __device__ inline void store(const Row& r, int64_t n, const float (&g)[W], const float (&u)[W],
+                               const Held<W>&) const {
+    float p[W];
+    product(r, n, g, u, p);
   }
 };
 
@@ -331,29 +364,55 @@ struct ActGradEpilogue {
   T* dgu;
   int64_t width;
   int32_t act;
-  struct Held {
-    Raw<T, 4> g, u;
+  struct Row {
+    const T* gu;
+    T* dgu;
   };
-  __device__ inline Held held(int64_t row, int64_t n) const {
-    return {load_part4(gu + row * 2 * width + n, width - n),
-            load_part4(gu + (row * 2 + 1) * width + n, width - n)};
+  template <int W>
+  struct Held {
+    Span<T, W> g, u;
+  };
+  __device__ inline Row row(int64_t r) const {
+    return {gu + r * 2 * width, dgu + r * 2 * width};
   }
-  __device__ inline void gradients(f32x4 da, const Held& h, f32x4& dg, f32x4& du) const {
+  template <int W>
+  __device__ inline Held<W> held(const Row& r, int64_t n) const {
+    return {load_span<W>(r.gu + n, width - n), load_span<W>(r.gu + width + n, width - n)};
+  }
+  template <int W>
+  __device__ inline void gradients(const float (&da)[W], const Held<W>& h, float (&dg)[W],
+                                   float (&du)[W]) const {
+    float g[W], f[W], slope[W];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const ActValue f = act_value<T>(act, h.g.get(i));
-      dg[i] = da[i] * h.u.get(i) * f.slope;
-      du[i] = da[i] * f.a;
+    for (int i = 0; i < W; ++i) g[i] = h.g.get(i);
+    activate<T>(act, g, f, slope);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      dg[i] = da[i] * h.u.get(i) * slope[i];
+      du[i] = da[i] * f[i];
     }
   }
-  __device__ inline void operator()(int64_t row, int64_t n, f32x4 da, const Held& h) const {
-    const int64_t have = width - n;
-    f32x4 dg, du;
+  template <int W>
+  __device__ inline void store(const Row& r, int64_t n, const float (&da)[W],
+                               const Held<W>& h) const {
+    float dg[W], du[W];
     gradients(da, h, dg, du);
-    store4(dgu + row * 2 * width + n, dg, have);
-    store4(dgu + (row * 2 + 1) * width + n, du, have);
+    store_span(r.dgu + n, dg, width - n);
+    store_span(r.dgu + width + n, du, width - n);
   }
 };
+
+// Weight gradients: the expert's matrices, or the parts' sums, [expert][part].
+template <class Out>
+struct WeightEpilogue {
+  Out* out[2];
+};
+
+// Four results of a matrix instruction, or of two whose columns follow each other.
+__device__ inline void put4(float* v, f32x4 x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = x[i];
+}
 
 // ---------------------------------------------------------------- matrix steps
 template <class T>

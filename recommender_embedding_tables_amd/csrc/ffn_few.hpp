@@ -139,10 +139,16 @@ __device__ inline void few_rows(const RowTile& t, const T* __restrict__ A,
     }
     const int64_t m = m0 + i * 16 + i16, n = n0 + q * 4;
     if (m >= t.count || n >= N) continue;
-    if constexpr (Epilogue::kDual)
-      epilogue(t.first + m, n, sum[0], sum[1], {});
-    else
-      epilogue(t.first + m, n, sum[0], {});
+    const typename Epilogue::Row row = epilogue.row(t.first + m);
+    const auto held = epilogue.template held<4>(row, n);
+    float v[4], u[4];
+    put4(v, sum[0]);
+    if constexpr (Epilogue::kDual) {
+      put4(u, sum[1]);
+      epilogue.store(row, n, v, u, held);
+    } else {
+      epilogue.store(row, n, v, held);
+    }
   }
 }
 

@@ -51,13 +51,13 @@ __global__ __launch_bounds__(256) void k_ffn_add_parts(const float* __restrict__
   const int64_t e = v / per, i = (v - e * per) * 4;
   if (e >= experts) return;
   const float* p = sums + e * parts * size + i;
-  f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+  float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (uint32_t k = 0; k < parts; ++k) {
-    const Raw<float> v4 = load_part4(p + k * size, size - i);
+    const Span<float, 4> v4 = load_span<4>(p + k * size, size - i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) t[j] += v4.get(j);
   }
-  store4(out + e * size + i, t, size - i);
+  store_span(out + e * size + i, t, size - i);
 }
 
 // The 256 x 256 tiles hold offsets of 32 bits: those of 256 rows, of 64 rows of the

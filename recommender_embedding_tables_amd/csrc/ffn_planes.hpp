@@ -33,7 +33,7 @@ __device__ inline void cut_planes(float a, float b, uint32_t (&w)[3]) {
 }
 
 // The planes of the first `have` of four values, then zeros up to `to` of them.
-__device__ inline void store_planes4(const Planes& o, int64_t at, f32x4 v, int64_t have,
+__device__ inline void store_planes4(const Planes& o, int64_t at, float (&v)[4], int64_t have,
                                      int64_t to) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = i < have ? v[i] : 0.0f;
@@ -104,39 +104,53 @@ __global__ __launch_bounds__(256) inline void k_ffn_cut(const Cuts c) {
 }
 
 // ---------------------------------------------------------------- epilogues
-// Both also cover the columns that pad a row of planes.
-struct ActPlanesEpilogue {
-  static constexpr bool kDual = true;
-  ActEpilogue<float> values;
-  Planes a;
-  __device__ inline int64_t columns() const { return a.ld; }
-  typedef NothingHeld Held;
-  __device__ inline Held held(int64_t, int64_t) const { return {}; }
-  __device__ inline void operator()(int64_t row, int64_t n, f32x4 g, f32x4 u, Held) const {
-    const int64_t have = values.width - n;
-    const f32x4 p = values.product(row, n, g, u);
-    store_planes4(a, row * a.ld + n, p, have, a.ld - n);
+// All also cover the columns that pad a row of planes.
+struct ActPlanesEpilogue : ActEpilogue<float> {
+  Planes planes;  // of a
+  struct Row {
+    ActEpilogue<float>::Row values;
+    int64_t at;
+  };
+  __device__ inline int64_t columns() const { return planes.ld; }
+  __device__ inline Row row(int64_t r) const {
+    return {ActEpilogue<float>::row(r), r * planes.ld};
+  }
+  __device__ inline NothingHeld held4(const Row&, int64_t) const { return {}; }
+  __device__ inline void store4(const Row& r, int64_t n, const float (&g)[4], const float (&u)[4],
+                                const NothingHeld&) const {
+    float p[4];
+    product(r.values, n, g, u, p);
+    store_planes4(planes, r.at + n, p, width - n, planes.ld - n);
   }
 };
 
-struct ActGradPlanesEpilogue {
-  static constexpr bool kDual = false;
-  ActGradEpilogue<float> values;  // its dgu is not written
-  Planes dgu;
-  __device__ inline int64_t columns() const { return values.width + dgu.ld - 2 * values.width; }
-  typedef ActGradEpilogue<float>::Held Held;
-  __device__ inline Held held(int64_t row, int64_t n) const { return values.held(row, n); }
-  __device__ inline void operator()(int64_t row, int64_t n, f32x4 da, const Held& h) const {
-    const int64_t width = values.width, have = width - n;
-    f32x4 dg, du;
-    values.gradients(da, h, dg, du);
-    store_planes4(dgu, row * dgu.ld + n, dg, have, have);
-    store_planes4(dgu, row * dgu.ld + width + n, du, have, dgu.ld - width - n);
+struct ActGradPlanesEpilogue : ActGradEpilogue<float> {
+  Planes planes;  // of dgu, which is not stored itself
+  struct Row {
+    ActGradEpilogue<float>::Row values;
+    int64_t at;
+  };
+  __device__ inline int64_t columns() const { return planes.ld - width; }
+  __device__ inline Row row(int64_t r) const {
+    return {ActGradEpilogue<float>::row(r), r * planes.ld};
+  }
+  __device__ inline Held<4> held4(const Row& r, int64_t n) const { return held<4>(r.values, n); }
+  __device__ inline void store4(const Row& r, int64_t n, const float (&da)[4],
+                                const Held<4>& h) const {
+    float dg[4], du[4];
+    gradients(da, h, dg, du);
+    store_planes4(planes, r.at + n, dg, width - n, width - n);
+    store_planes4(planes, r.at + width + n, du, width - n, planes.ld - width - n);
   }
 };
 
 struct StorePlanesEpilogue : StoreEpilogue<float> {
   __device__ inline int64_t columns() const { return width; }
+  __device__ inline NothingHeld held4(const Row&, int64_t) const { return {}; }
+  __device__ inline void store4(const Row& r, int64_t n, const float (&v)[4],
+                                const NothingHeld& h) const {
+    store(r, n, v, h);
+  }
 };
 
 // ---------------------------------------------------------------- product
@@ -349,20 +363,22 @@ __global__ __launch_bounds__(OM * 4) void k_ffn_rows_planes(
   for (int i = 0; i < FM; ++i) {
     const int64_t m = m0 + wm + i * 16 + (lane & 15u);
     if (m >= t.count) continue;
-    typename Epilogue::Held held[kOut];
+    const typename Epilogue::Row row = epilogue.row(first + m);
+    const auto col = [&](int j) { return n0 + wn + j * 16 + (lane >> 4) * 4; };
+    decltype(epilogue.held4(row, 0)) held[kOut];
+#pragma unroll
+    for (int j = 0; j < kOut; ++j) held[j] = epilogue.held4(row, col(j) < N ? col(j) : N - 1);
 #pragma unroll
     for (int j = 0; j < kOut; ++j) {
-      const int64_t n = n0 + wn + j * 16 + (lane >> 4) * 4;
-      held[j] = epilogue.held(first + m, n < N ? n : N - 1);
-    }
-#pragma unroll
-    for (int j = 0; j < kOut; ++j) {
-      const int64_t n = n0 + wn + j * 16 + (lane >> 4) * 4;
-      if (n >= epilogue.columns()) continue;
-      if constexpr (Epilogue::kDual)
-        epilogue(first + m, n, acc[i][j], acc[i][j + FN / 2], held[j]);
-      else
-        epilogue(first + m, n, acc[i][j], held[j]);
+      if (col(j) >= epilogue.columns()) continue;
+      float v[4], u[4];
+      put4(v, acc[i][j]);
+      if constexpr (Epilogue::kDual) {
+        put4(u, acc[i][j + FN / 2]);
+        epilogue.store4(row, col(j), v, u, held[j]);
+      } else {
+        epilogue.store4(row, col(j), v, held[j]);
+      }
     }
   }
 }
@@ -398,7 +414,7 @@ __global__ __launch_bounds__(OM * 4) void k_ffn_weights_planes(
                (int32_t)((K + kHalfK - 1) / kHalfK), Fragments<false, OM>(wm, lane),
                Fragments<false, kTileO>(wn, lane), [](int j) { return (uint32_t)(j * 16); }, lds,
                acc);
-  const int64_t matrix = (int64_t)t.expert * w.parts + t.part;
+  Out* to = out.out[t.product] + ((int64_t)t.expert * w.parts + t.part) * M * N;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int64_t m = m0 + wm + i * 16 + (lane & 15u);
@@ -406,7 +422,9 @@ __global__ __launch_bounds__(OM * 4) void k_ffn_weights_planes(
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const int64_t n = n0 + wn + j * 16 + (lane >> 4) * 4;
-      if (n < N) out(t.product, matrix, M, N, m, n, acc[i][j]);
+      float v[4];
+      put4(v, acc[i][j]);
+      if (n < N) store_span(to + m * N + n, v, N - n);
     }
   }
 }

@@ -253,15 +253,20 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ffn_rows(
   for (int i = 0; i < 4; ++i) {
     const int64_t m = m0 + wm + i * 16 + (lane & 15u);
     if (m >= t.count) continue;
+    const typename Epilogue::Row row = epilogue.row(first + m);
 #pragma unroll
     for (int j = 0; j < (Epilogue::kDual ? 2 : 4); ++j) {
       const int64_t n = n0 + wn + j * 16 + (lane >> 4) * 4;
       if (n >= N) continue;
-      const typename Epilogue::Held held = epilogue.held(first + m, n);
-      if constexpr (Epilogue::kDual)
-        epilogue(first + m, n, acc[i][j], acc[i][j + 2], held);
-      else
-        epilogue(first + m, n, acc[i][j], held);
+      const auto held = epilogue.template held<4>(row, n);
+      float v[4], u[4];
+      put4(v, acc[i][j]);
+      if constexpr (Epilogue::kDual) {
+        put4(u, acc[i][j + 2]);
+        epilogue.store(row, n, v, u, held);
+      } else {
+        epilogue.store(row, n, v, held);
+      }
     }
   }
 }
@@ -286,7 +291,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ffn_weights(const WeightPro
   const uint32_t wm = (wave & 1u) * 64u, wn = (wave >> 1) * 64u;
   f32x4 acc[4][4];
   Product::run(a, b, K, M, N, wm, [&](int j) { return wn + j * 16u; }, lds, acc);
-  const int64_t matrix = (int64_t)t.expert * w.parts + t.part;
+  Out* to = out.out[t.product] + ((int64_t)t.expert * w.parts + t.part) * M * N;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t m = m0 + wm + i * 16 + (lane & 15u);
@@ -294,7 +299,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ffn_weights(const WeightPro
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t n = n0 + wn + j * 16 + (lane >> 4) * 4;
-      if (n < N) out(t.product, matrix, M, N, m, n, acc[i][j]);
+      float v[4];
+      put4(v, acc[i][j]);
+      if (n < N) store_span(to + m * N + n, v, N - n);
     }
   }
 }

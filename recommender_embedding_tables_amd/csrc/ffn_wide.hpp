@@ -64,12 +64,16 @@ __device__ inline void stage_landed() {
 // The eight 16-byte pieces of a KC row of 128 bytes are turned by the row, so that
 // the 16 lanes a read serves at once (ffn_tiles.hpp) meet no bank twice.
 __device__ inline uint32_t wide_kc_turn(uint32_t row) { return (row >> 1) & 7u; }
+// The same for the columns' operand, whose fragments take 4 of every 8 indexes.
+__device__ inline uint32_t wide_kc_pair_turn(uint32_t row) {
+  return ((row >> 1) & 1u) | ((row >> 2) & 6u);
+}
 
 // Loads of one operand straight into LDS: THREADS threads, kVecs vectors each a
 // slot.  The place of a vector in LDS is the thread's own (the hardware puts a
 // wave's 64 vectors one after another), so the turning is in the address read from;
 // it is the same for all of a thread's vectors.
-template <bool KC, int THREADS>
+template <bool KC, bool PAIRS, int THREADS>
 struct WideLoads {
   static constexpr int kVecs = kWideValues / 8 / THREADS;
   static constexpr int kRows = THREADS / (KC ? 8 : kWideO / 8);  // from a vector to the next
@@ -82,7 +86,8 @@ struct WideLoads {
   static __device__ inline uint32_t first_k() {
     uint32_t t = threadIdx.x;
     asm volatile("" : "+v"(t));
-    return KC ? ((t & 7u) ^ wide_kc_turn(t >> 3)) * 8 : t / (kWideO / 8);
+    if (!KC) return t / (kWideO / 8);
+    return ((t & 7u) ^ (PAIRS ? wide_kc_pair_turn(t >> 3) : wide_kc_turn(t >> 3))) * 8;
   }
 
   // row(i): offset in values of the operand's index i, below 2^31 (KC)
@@ -156,20 +161,57 @@ struct WideFragments {
   }
 };
 
+// The columns' fragments go in pairs that share 32 columns: the first takes columns
+// 8 q to 8 q + 3 of them and the second the next four, so that a lane's results of
+// both are eight neighbouring columns of a row.  (The reads of OC pairs meet two
+// lanes in a bank.)
+template <bool KC>
+struct WidePairs {
+  uint32_t base[2], turn;
+  __device__ inline WidePairs(uint32_t o0, uint32_t lane) {
+    const uint32_t i = lane & 15u, q = lane >> 4;
+    if (KC) {
+      const uint32_t r = (i >> 2) * 8 + (i & 3u);
+#pragma unroll
+      for (uint32_t h = 0; h < 2; ++h)
+        base[h] = (o0 + r) * (kWideK * 2) + (((h * 4 + q) ^ wide_kc_pair_turn(r)) << 4);
+      turn = 0;
+    } else {
+      const uint32_t k = q * 8 + (i >> 2);
+      base[0] = k * kWideO * 2;
+      base[1] = base[0] + kHalfK * kWideO * 2;
+      turn = (o0 * 2 + (i & 3u) * 16) ^ (oc_turn(k) << 4);
+    }
+  }
+  // fragment `second` of the pair that begins at o0 + delta
+  __device__ inline i16x8 read(uint32_t slot, int half, uint32_t delta, int second) const {
+    typedef __attribute__((address_space(3))) i16x8 lds_i16x8;
+    typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+    if (KC)
+      return *(const lds_i16x8*)(uintptr_t)(base[half] + slot +
+                                             (delta + second * 4) * (kWideK * 2));
+    const uint32_t at = (turn ^ (delta * 2)) + (base[half] + slot) + second * 8;
+    const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(uintptr_t)at);
+    const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_i16x4*)(uintptr_t)(at + 4 * kWideO * 2));
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+
 template <class T, bool A_KC, bool B_KC, int WM, int WN>
 struct WideProduct {
   static constexpr int kThreads = 64 * WM * WN;
   static constexpr int FM = kWideO / WM / 16, FN = kWideO / WN / 16;
-  typedef WideLoads<A_KC, kThreads> LoadsA;
-  typedef WideLoads<B_KC, kThreads> LoadsB;
+  typedef WideLoads<A_KC, false, kThreads> LoadsA;
+  typedef WideLoads<B_KC, true, kThreads> LoadsB;
   static constexpr int kLoads = LoadsA::kVecs + LoadsB::kVecs;
 
   // acc[fm][fn] over K; step_a, step_b: bytes from one slot to the next;
-  // delta_b(fn): of the wave's fragment fn
+  // delta_b(p): of the wave's pair p of column fragments
   template <class Delta>
   __device__ static inline void run(LoadsA& a, LoadsB& b, int64_t step_a, int64_t step_b,
                                     int64_t K, const WideFragments<A_KC>& at_a,
-                                    const WideFragments<B_KC>& at_b, Delta delta_b,
+                                    const WidePairs<B_KC>& at_b, Delta delta_b,
                                     uint16_t* lds, f32x4 (&acc)[FM][FN]) {
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -198,7 +240,7 @@ struct WideProduct {
     if (steps > 2) stage_landed<kLoads>();
     else stage_landed<0>();
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[0][j] = at_b.read(first + kOperand, 0, delta_b(j));
+    for (int j = 0; j < FN; ++j) fb[0][j] = at_b.read(first + kOperand, 0, delta_b(j / 2), j & 1);
 #pragma unroll
     for (int i = 0; i < FM; ++i) fa[0][i] = at_a.read(first, 0, i * 16);
     // A step's matrix instructions, and between them the reads of the next step's
@@ -210,7 +252,7 @@ struct WideProduct {
       for (int i = 0; i < FM; ++i) {
 #pragma unroll
         for (int r = i * kReads; r < (i + 1) * kReads; ++r) {
-          if (r < FN) fb[next][r] = at_b.read(from + kOperand, next, delta_b(r));
+          if (r < FN) fb[next][r] = at_b.read(from + kOperand, next, delta_b(r / 2), r & 1);
           else if (r < FN + FM) fa[next][r - FN] = at_a.read(from, next, (r - FN) * 16);
         }
         if (now == 1)
@@ -264,27 +306,23 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ffn_rows_wide(
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
   const uint32_t wm = wave % WM * (kWideO / WM), wn = wave / WM * (kCols / WN);
   const WideFragments<true> at_a(wm, lane);
-  const WideFragments<B_KC> at_b(wn, lane);
+  const WidePairs<B_KC> at_b(wn, lane);
   f32x4 acc[FM][FN];
   Product::run(a, b, kWideK * 2, B_KC ? kWideK * 2 : (int64_t)kWideK * 2 * N,
                K, at_a, at_b,
-               [](int j) {
-                 return Epilogue::kDual
-                            ? (uint32_t)(j % (FN / 2) * 16 + j / (FN / 2) * kCols)
-                            : (uint32_t)(j * 16);
-               },
-               lds, acc);
+               [](int p) { return (uint32_t)(p * (Epilogue::kDual ? kCols : 32)); }, lds, acc);
   // What the epilogue reads for a row is on its way while the row before is
   // stored; rows and columns past the end read inside the matrix.
-  constexpr int kOut = Epilogue::kDual ? FN / 2 : FN;
-  typename Epilogue::Held held[2][kOut];
+  constexpr int kPairs = Epilogue::kDual ? FN / 4 : FN / 2;
+  typename Epilogue::template Held<8> held[2][kPairs];
   const auto row_of = [&](int i) { return m0 + wm + i * 16 + (lane & 15u); };
-  const auto col_of = [&](int j) { return n0 + wn + j * 16 + (lane >> 4) * 4; };
+  const auto col_of = [&](int p) { return n0 + wn + p * 32 + (lane >> 4) * 8; };
   const auto hold = [&](int i) {
     const int64_t m = row_of(i) < t.count ? row_of(i) : t.count - 1;
+    const typename Epilogue::Row row = epilogue.row(first + m);
 #pragma unroll
-    for (int j = 0; j < kOut; ++j)
-      held[i & 1][j] = epilogue.held(first + m, col_of(j) < N ? col_of(j) : N - 1);
+    for (int p = 0; p < kPairs; ++p)
+      held[i & 1][p] = epilogue.template held<8>(row, col_of(p) < N ? col_of(p) : N - 1);
   };
   hold(0);
 #pragma unroll
@@ -292,14 +330,21 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ffn_rows_wide(
     if (i + 1 < FM) hold(i + 1);
     const int64_t m = row_of(i);
     if (m >= t.count) continue;
+    const typename Epilogue::Row row = epilogue.row(first + m);
 #pragma unroll
-    for (int j = 0; j < kOut; ++j) {
-      const int64_t n = col_of(j);
+    for (int p = 0; p < kPairs; ++p) {
+      const int64_t n = col_of(p);
       if (n >= N) continue;
-      if constexpr (Epilogue::kDual)
-        epilogue(first + m, n, acc[i][j], acc[i][j + FN / 2], held[i & 1][j]);
-      else
-        epilogue(first + m, n, acc[i][j], held[i & 1][j]);
+      float v[8], u[8];
+      put4(v, acc[i][2 * p]);
+      put4(v + 4, acc[i][2 * p + 1]);
+      if constexpr (Epilogue::kDual) {
+        put4(u, acc[i][2 * p + FN / 2]);
+        put4(u + 4, acc[i][2 * p + FN / 2 + 1]);
+        epilogue.store(row, n, v, u, held[i & 1][p]);
+      } else {
+        epilogue.store(row, n, v, held[i & 1][p]);
+      }
     }
   }
 }
@@ -326,16 +371,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_ffn_weights_wide(
   f32x4 acc[FM][FN];
   Product::run(a, b, (int64_t)kWideK * 2 * M, (int64_t)kWideK * 2 * N,
                K, WideFragments<false>(wm, lane),
-               WideFragments<false>(wn, lane), [](int j) { return (uint32_t)(j * 16); }, lds, acc);
-  const int64_t matrix = (int64_t)t.expert * w.parts + t.part;
+               WidePairs<false>(wn, lane), [](int p) { return (uint32_t)(p * 32); }, lds, acc);
+  Out* to = out.out[t.product] + ((int64_t)t.expert * w.parts + t.part) * M * N;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int64_t m = m0 + wm + i * 16 + (lane & 15u);
     if (m >= M) continue;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int64_t n = n0 + wn + j * 16 + (lane >> 4) * 4;
-      if (n < N) out(t.product, matrix, M, N, m, n, acc[i][j]);
+    for (int p = 0; p < FN / 2; ++p) {
+      const int64_t n = n0 + wn + p * 32 + (lane >> 4) * 8;
+      float v[8];
+      put4(v, acc[i][2 * p]);
+      put4(v + 4, acc[i][2 * p + 1]);
+      if (n < N) store_span(to + m * N + n, v, N - n);
     }
   }
 }
