@@ -199,19 +199,31 @@ inline dim3 tile_grid(int64_t blocks, int threads) {
 }
 
 // ---------------------------------------------------------------- activations
-// act(v) and its slope for N values (one choice of the activation for all).  16-bit
-// data takes the hardware's exponential and reciprocal (within a few 2^-23, far
-// below its own rounding).
+// act(v) and its slope for N values (one choice of the activation for all).
+//
+// e^-v as 2 to the power of -v log2(e) by the hardware.  The product's rounding
+// would be |v| 2^-24 of the result: below 16-bit data's own rounding, while fp32
+// takes it up again, e = the product's error with log2(e)'s second half, as
+// 2^(p + e) = 2^p (1 + e ln 2) within 2^-40.  1 / (1 + t) by the hardware's
+// reciprocal (1 ulp), for fp32 with one Newton step below 2^126.  The hardware gives 0
+// for results below 2^-126.
+template <class T>
+__device__ inline float exp_neg(float v) {
+  constexpr float kLog = 1.44269504088896340736f, kLow = 1.92596299112661746887e-8f;
+  const float p = v * -kLog;
+  const float t = __builtin_amdgcn_exp2f(p);
+  if constexpr (sizeof(T) == 2) return t;
+  if (!(__builtin_fabsf(p) < 126.0f)) return t;  // 0 or infinite, nearly or in fact, or a NaN
+  const float e = __builtin_fmaf(v, -kLow, __builtin_fmaf(v, -kLog, -p));
+  return __builtin_fmaf(t, e * 0.69314718055994530942f, t);
+}
+
 template <class T>
 __device__ inline void logistic(float v, float& s, float& rest) {  // s(v) and 1 - s(v)
-  float t;
-  if constexpr (sizeof(T) == 4) {
-    t = expf(-v);
-    s = 1.0f / (1.0f + t);
-  } else {
-    t = __builtin_amdgcn_exp2f(v * -1.44269504088896340736f);
-    s = __builtin_amdgcn_rcpf(1.0f + t);
-  }
+  const float t = exp_neg<T>(v), x = 1.0f + t;
+  s = __builtin_amdgcn_rcpf(x);
+  if constexpr (sizeof(T) == 4)
+    s = x < 0x1p126f ? __builtin_fmaf(__builtin_fmaf(-x, s, 1.0f), s, s) : s;
   rest = v > 0.0f ? t * s : 1.0f - s;  // 1 - s cancels where s is near 1
 }
 

@@ -60,15 +60,37 @@ __global__ __launch_bounds__(256) void k_ffn_add_parts(const float* __restrict__
   store_span(out + e * size + i, t, size - i);
 }
 
-// The 256 x 256 tiles hold offsets of 32 bits: those of 256 rows, of 64 rows of the
-// other operand, or of a projection behind the other.
-bool wide_offsets(int64_t K, int64_t N) { return K * N < (1ll << 30) && K + N < (1ll << 20); }
+// Whether a product of the groups' rows goes by tiles of 256 x 256 (ffn_wide.hpp): they
+// hold offsets of 32 bits (256 rows of one operand, 64 of the other, a projection behind
+// the other), take long to start and need enough blocks to fill the card (us of a
+// forward, against tiles of 128 x 128):
+//   8 experts, 512 x 1024: 512 rows each (128 blocks) 47, 44; 1024 (256 blocks) 52, 55
+//   1 expert, 3328 x 1664: 1024 rows (52 blocks) 110, 101; 4096 (208 blocks) 140, 238
+//   64 experts, 128 x 256: 4096 rows each 168, 144: two slots of k are too few
+constexpr int64_t kWideBlocks = 160, kWideLeastK = 256;
+bool wide_fits(int64_t K, int64_t N) {
+  return K >= kWideLeastK && K * N < (1ll << 30) && K + N < (1ll << 20);
+}
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-#ifndef FEW
-#define FEW 64
-#endif
+// Whether the forward's products go by ffn_few.hpp: each of its passes over the
+// weights serves 64 rows of an expert, and keeps up with the tiles while few blocks of
+// 128 columns would be at work (`tiles`), or few rows use what is read (us of a
+// forward, this kernel against tiles):
+//   bf16  1 expert, 3328 x 1664: 256 rows 77, 99; 512 rows 149, 98
+//         8 experts, 512 x 1024: 64 rows each 19, 35; 128 34, 36; 256 59, 37
+//         32 experts, 1664 x 1024: 8 rows each 81, 85; 16 90, 85; 32 117, 87
+//   fp32  1 expert, 3328 x 1664: 128 rows 93, 130; 256 189, 131
+//         32 experts, 1664 x 1024: 16 rows each 188, 241; 32 249, 251; 64 402, 245
+template <class T>
+bool by_few_rows(const Groups& g, int64_t hidden) {
+  const int64_t passes = (g.rows + kFewRows * g.experts - 1) / (kFewRows * g.experts);
+  const int64_t tiles = g.experts * ((hidden + 127) / 128);
+  return g.rows <= (sizeof(T) == 2 ? 16 : 32) * (int64_t)g.experts ||
+         passes * tiles <= (passes == 1 ? 128 : sizeof(T) == 2 ? 64 : 40);
+}
+
 // C = A B' over groups of few rows
 template <class T, class Epilogue>
 hipError_t few_rows_product(const Groups& g, const void* a, const void* b, int64_t K, int64_t N,
@@ -87,16 +109,13 @@ template <class T, bool B_KC, class Epilogue>
 hipError_t rows_product(const Groups& g, const void* a, const void* b, int64_t K, int64_t N,
                         int64_t b_stride, const Epilogue& epilogue, hipStream_t s) {
   if (g.rows == 0) return hipSuccess;
-  if constexpr (B_KC) {
-    if (g.rows <= FEW * (int64_t)g.experts)
-      return few_rows_product<T>(g, a, b, K, N, b_stride, epilogue, s);
-  }
   if constexpr (sizeof(T) == 2) {
-    if (K % 8 == 0 && (B_KC || N % 8 == 0) && on16(a) && on16(b) && wide_offsets(K, N)) {
-      constexpr int WM = 2, WN = 4;
-      const int64_t cols = Epilogue::kDual ? kWideO / 2 : kWideO;
-      const int64_t col_tiles = (N + cols - 1) / cols;
-      const int64_t blocks = blocks_of(row_tiles_bound(g, kWideO) * col_tiles, kRowChunk);
+    constexpr int WM = 2, WN = 4;
+    const int64_t cols = Epilogue::kDual ? kWideO / 2 : kWideO;
+    const int64_t col_tiles = (N + cols - 1) / cols;
+    const int64_t blocks = blocks_of(row_tiles_bound(g, kWideO) * col_tiles, kRowChunk);
+    if (K % 8 == 0 && (B_KC || N % 8 == 0) && on16(a) && on16(b) && wide_fits(K, N) &&
+        blocks >= kWideBlocks) {
       hipLaunchKernelGGL((k_ffn_rows_wide<T, B_KC, Epilogue, WM, WN>),
                          tile_grid(blocks, 64 * WM * WN), dim3(64 * WM * WN), 0, s, g,
                          static_cast<const T*>(a), static_cast<const T*>(b), K, N, b_stride,
@@ -113,15 +132,27 @@ hipError_t rows_product(const Groups& g, const void* a, const void* b, int64_t K
   return hipGetLastError();
 }
 
-#ifndef ONEROUND
-#define ONEROUND 192
-#endif
-#ifndef PLANES
-#define PLANES 128
-#endif
-// fp32 goes through planes where an expert has this many rows: its values then
-// enter more than one tile.
-bool by_planes(int64_t rows, int32_t experts) { return rows >= PLANES * (int64_t)experts; }
+// Whether fp32 goes through planes: while the middle has few blocks of 128 x 128 (of
+// tiles that cut their own values several on a CU hide each other's waits), more of
+// them where many rows share an expert's planes (us, planes against those tiles):
+//   forward   1 expert, 3327 x 1663: 1024 rows (104 blocks) 212, 288
+//             1 expert, 479 x 1000: 4096 rows (256 blocks) 99, 112
+//             16 experts, 479 x 640: 128 rows each (80 blocks) 70, 73; 256 (160) 101, 88
+//   backward  1 expert, 3327 x 1663: 1024 rows 398, 648; 4096 (416 blocks) 1410, 1642
+//             16 experts, 479 x 640: 256 rows each (160 blocks) 174, 195; 512 (320) 295, 256
+//             8 experts, 479 x 640: 1024 rows each (320 blocks) 250, 252
+//             32 experts, 1664 x 1024: 8 rows each (256 blocks) 841, 475
+struct PlanesRule {
+  int64_t blocks;                  // fewer than this
+  int64_t long_blocks, long_rows;  // or up to this many, of experts with so many rows
+};
+constexpr PlanesRule kForwardPlanes{112, 256, 2048}, kBackwardPlanes{256, 512, 1024};
+bool by_planes(int64_t rows, int32_t experts, int64_t hidden, const PlanesRule& r) {
+  // the groups' largest number of row tiles, whatever the capacity
+  const int64_t used = rows < experts ? rows : experts;
+  const int64_t blocks = (rows + used * 127) / 128 * ((hidden + 127) / 128);
+  return blocks < r.blocks || (blocks <= r.long_blocks && rows >= r.long_rows * experts);
+}
 
 // Hands out the workspace from its start.
 struct Space {
@@ -157,7 +188,9 @@ hipError_t rows_product_planes(const Groups& g, const Planes& a, const Planes& b
   const int64_t cols = Epilogue::kDual ? kTileO / 2 : kTileO;
   const int64_t col_tiles = (N + cols - 1) / cols;
   const int64_t blocks = blocks_of(row_tiles_bound(g, 128) * col_tiles, kRowChunk);
-  if (blocks <= ONEROUND) {
+  // 64 rows a block where 128 leave CUs without one (4096 x 479 from 1000: 36 us
+  // against 49)
+  if (blocks <= 192) {
     const int64_t half = blocks_of(row_tiles_bound(g, 64) * col_tiles, kRowChunk);
     hipLaunchKernelGGL((k_ffn_rows_planes<B_KC, Epilogue, 64>), tile_grid(half, 256), dim3(256),
                        0, s, g, a, b, N, b_rows, (uint32_t)col_tiles, epilogue);
@@ -175,6 +208,10 @@ hipError_t launch_weights(WeightProducts<T>& w, const WeightPlanes* planes,
   bool wide = sizeof(T) == 2;
   for (int p = 0; p < 2; ++p)
     wide = wide && w.M[p] % 8 == 0 && w.N[p] % 8 == 0 && on16(w.A[p]) && on16(w.B[p]);
+  // (1 expert, 512 x 1024, 24 tiles: the backward of 512 rows 106 us with these tiles,
+  // 94 with 128 x 128; 8 experts, 480 x 640, 128 tiles: 85 and 101)
+  wide = wide && w.groups.experts * (tiles_of(w.M[0], w.N[0], kWideO) +
+                                     tiles_of(w.M[1], w.N[1], kWideO)) >= 100;
   const int64_t tile = wide ? kWideO : kTileO;
   int64_t tiles = 0;
   for (int p = 0; p < 2; ++p) {
@@ -276,7 +313,7 @@ hipError_t backward_planes(const GatedFfn& f, const void* gu, const void* a, con
 template <class T>
 size_t ffn_workspace_bytes_t(int64_t rows, int32_t experts, int64_t dim, int64_t hidden) {
   size_t n = dgu_bytes(rows, hidden, sizeof(T));
-  if (sizeof(T) == 4 && by_planes(rows, experts))
+  if (sizeof(T) == 4 && by_planes(rows, experts, hidden, kBackwardPlanes))
     n = 2 * planes_bytes(rows, dim) + planes_bytes(rows, hidden) +
         planes_bytes(rows, 2 * hidden) + planes_bytes(experts * 2 * hidden, dim) +
         planes_bytes(experts * dim, hidden);
@@ -285,23 +322,29 @@ size_t ffn_workspace_bytes_t(int64_t rows, int32_t experts, int64_t dim, int64_t
 
 template <class T>
 hipError_t ffn_forward_t(const GatedFfn& f, void* gu, void* a, void* y, char* ws, hipStream_t s) {
-  if constexpr (sizeof(T) == 4)
-    if (by_planes(f.rows, f.experts)) return forward_planes(f, gu, a, y, ws, s);
   const int64_t D = f.dim, F = f.hidden;
   const Groups g{f.offsets, f.rows, f.capacity, f.experts};
-  const hipError_t e = rows_product<T, true>(
-      g, f.x, f.w_in, D, F, 2 * F * D,
-      ActEpilogue<T>{static_cast<T*>(gu), static_cast<T*>(a), F, f.act}, s);
+  const ActEpilogue<T> middle{static_cast<T*>(gu), static_cast<T*>(a), F, f.act};
+  const StoreEpilogue<T> end{static_cast<T*>(y), D};
+  if (g.rows == 0) return hipSuccess;
+  if (by_few_rows<T>(g, F)) {
+    const hipError_t e = few_rows_product<T>(g, f.x, f.w_in, D, F, 2 * F * D, middle, s);
+    if (e != hipSuccess) return e;
+    return few_rows_product<T>(g, a, f.w_out, F, D, D * F, end, s);
+  }
+  if constexpr (sizeof(T) == 4)
+    if (by_planes(f.rows, f.experts, F, kForwardPlanes))
+      return forward_planes(f, gu, a, y, ws, s);
+  const hipError_t e = rows_product<T, true>(g, f.x, f.w_in, D, F, 2 * F * D, middle, s);
   if (e != hipSuccess) return e;
-  return rows_product<T, true>(g, a, f.w_out, F, D, D * F,
-                               StoreEpilogue<T>{static_cast<T*>(y), D}, s);
+  return rows_product<T, true>(g, a, f.w_out, F, D, D * F, end, s);
 }
 
 template <class T>
 hipError_t ffn_backward_t(const GatedFfn& f, const void* gu, const void* a, const void* dy,
                           void* dx, void* dw_in, void* dw_out, char* ws, hipStream_t s) {
   if constexpr (sizeof(T) == 4)
-    if (by_planes(f.rows, f.experts))
+    if (f.rows && by_planes(f.rows, f.experts, f.hidden, kBackwardPlanes))
       return backward_planes(f, gu, a, dy, dx, dw_in, dw_out, ws, s);
   const int64_t D = f.dim, F = f.hidden;
   const Groups g{f.offsets, f.rows, f.capacity, f.experts};

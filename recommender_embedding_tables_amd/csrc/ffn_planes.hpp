@@ -358,26 +358,33 @@ __global__ __launch_bounds__(OM * 4) void k_ffn_rows_planes(
                             : (uint32_t)(j * 16);
                },
                lds, acc);
+  // What the epilogue reads is on its way before the first row is stored; rows and
+  // columns past the end read inside the matrix.
   constexpr int kOut = Epilogue::kDual ? FN / 2 : FN;
+  const auto row_of = [&](int i) { return m0 + wm + i * 16 + (lane & 15u); };
+  const auto col_of = [&](int j) { return n0 + wn + j * 16 + (lane >> 4) * 4; };
+  decltype(epilogue.held4(epilogue.row(0), 0)) held[FM][kOut];
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int64_t m = m0 + wm + i * 16 + (lane & 15u);
-    if (m >= t.count) continue;
-    const typename Epilogue::Row row = epilogue.row(first + m);
-    const auto col = [&](int j) { return n0 + wn + j * 16 + (lane >> 4) * 4; };
-    decltype(epilogue.held4(row, 0)) held[kOut];
+    const auto row = epilogue.row(first + (row_of(i) < t.count ? row_of(i) : t.count - 1));
 #pragma unroll
-    for (int j = 0; j < kOut; ++j) held[j] = epilogue.held4(row, col(j) < N ? col(j) : N - 1);
+    for (int j = 0; j < kOut; ++j)
+      held[i][j] = epilogue.held4(row, col_of(j) < N ? col_of(j) : N - 1);
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    if (row_of(i) >= t.count) continue;
+    const typename Epilogue::Row row = epilogue.row(first + row_of(i));
 #pragma unroll
     for (int j = 0; j < kOut; ++j) {
-      if (col(j) >= epilogue.columns()) continue;
+      if (col_of(j) >= epilogue.columns()) continue;
       float v[4], u[4];
       put4(v, acc[i][j]);
       if constexpr (Epilogue::kDual) {
         put4(u, acc[i][j + FN / 2]);
-        epilogue.store4(row, col(j), v, u, held[j]);
+        epilogue.store4(row, col_of(j), v, u, held[i][j]);
       } else {
-        epilogue.store4(row, col(j), v, held[j]);
+        epilogue.store4(row, col_of(j), v, held[i][j]);
       }
     }
   }

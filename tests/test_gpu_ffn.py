@@ -203,6 +203,44 @@ def test_activations(act, scale, kind):
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("act", list(ACTS))
+def test_activations_far_out(act, kind):
+    """Gate pre-activations from 1e-3 to beyond the exponential's range, infinite and NaN,
+    through the backward, whose da and u are 1: dw_in of one row is dgu itself."""
+    t = TYPES[kind]
+    top = 1e4 if kind == "f16" else 1e30
+    far = torch.logspace(-3, np.log10(top), 118, dtype=torch.float64, device=DEV)
+    near = torch.linspace(-20, 20, 81, dtype=torch.float64, device=DEV)
+    g = torch.cat([far, -far, near, torch.tensor([float("inf"), float("-inf"), float("nan")],
+                                                 dtype=torch.float64, device=DEV)])
+    F = g.numel()
+    c = Case([1], 0, 0, 8, F, kind, act)
+    c.gu = torch.cat([g.to(t), torch.ones(F, dtype=t, device=DEV)]).view(1, -1)
+    c.x.fill_(1.0)
+    c.dy.fill_(0.0)
+    c.dy[0, 0] = 1.0
+    c.w_out.fill_(1.0)
+    _, dw_in, _ = c.backward()
+    got = dw_in[0, :, 0].double()
+    f, slope = act64(act, c.gu[0, :F].double())
+    lim = act_rel(c.gu[0, :F].double())
+    ok = torch.isfinite(g)
+    big = torch.finfo(t).max
+    for name, v, ref in (("dg", got[:F], slope), ("du", got[F:], f)):
+        r = ref[ok]
+        # the slopes' parts are below 1.2; a slope 1 - s s' of a far gate may be off by them.
+        # The hardware's exponential and reciprocal give 0 below 2^-126, which v (below
+        # 104 where fp32 still holds e^v) makes |v| 2^-126 of v s and of its slope.
+        v0 = c.gu[0, :F].double()[ok].abs().clamp(max=104)
+        off = (lim[ok] * (r.abs() + (1.2 if name == "dg" else 0)) + 2 * half(t) * r.abs() + TINY[t]
+               + (1 + v0) * 2.0 ** -126)
+        assert ((v[ok] - r).abs() <= off)[r.abs() < big].all(), name
+        assert v[-1].isnan() or act == "relu" and name == "dg", name
+    if act == "sigmoid":
+        assert got[F:][F - 3:F - 1].tolist() == [1.0, 0.0]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
 @pytest.mark.parametrize("rows,dim,hidden", [(1, 64, 128), (300, 351, 100), (37, 8, 9),
                                              (1030, 256, 264)])
 def test_dense_without_offsets(rows, dim, hidden, kind):
