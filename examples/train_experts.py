@@ -8,10 +8,13 @@ of all of them (dense parameters and the touched rows of the tables) is clipped
 once, and the step follows.
 
     python examples/train_experts.py [--steps 30] [--batch 4096] [--dim 64]
+                                     [--hidden 512] [--dropout 0.1]
 
 The step: prepare and look up (emb_bag_prepare, emb_bag_forward_prepared), route
 (emb_expert_sort, _dispatch, _combine), join (emb_gated_norm_forward), their
-gradients in reverse, the tables' deduplicated gradients
+gradients in reverse, with experts of one matrix each or, given a hidden width, gated
+feed-forward blocks (emb_gated_ffn_forward, _backward), dropout of what they
+return (emb_dropout), the tables' deduplicated gradients
 (emb_bag_grad_reduce_prepared), the clip (emb_clip_grad_norm), and the Adagrad
 step of the rows with the clipped sums (emb_bag_adagrad_reduced_prepared).
 """
@@ -28,19 +31,22 @@ from recommender_embedding_tables_amd import embtab as eb  # noqa: E402
 GATE = eb.EMB_GATE_ROW | eb.EMB_GATE_SIGMOID
 NORM_EPS, ADAGRAD_EPS = 1e-6, 1e-8
 PARAMS = ("router", "experts", "gate", "post", "scale", "pre", "head")
+FFN_PARAMS = ("router", "w_in", "w_out", "gate", "post", "scale", "pre", "head")
 
 
 class Model:
     """Parameters, buffers and workspaces, allocated once for a batch size."""
 
     def __init__(self, rows, dim, batch, experts=8, topk=2, max_norm=1.0, lr=0.05, seed=1,
-                 device="cuda"):
+                 device="cuda", hidden=0, dropout=0.0):
         self.tabs = eb.EmbTables(rows, dim, seed=seed, device=device)
         self.batch, self.experts, self.topk = batch, experts, topk
         self.width = width = self.tabs.T * dim
         self.capacity = -(-batch * topk * 5 // (4 * experts))  # 1.25 times an even share
         self.rows_m = experts * self.capacity
         self.max_norm, self.lr = max_norm, lr
+        self.hidden, self.dropout = hidden, dropout
+        self.names = FFN_PARAMS if hidden else PARAMS
         g = torch.Generator(device=device)
         g.manual_seed(seed)
 
@@ -48,12 +54,17 @@ class Model:
             return torch.randn(*shape, generator=g, device=device) / shape[-2] ** 0.5
 
         ones = torch.ones(width, device=device)
-        self.p = {"router": normal(width, experts), "experts": normal(experts, width, width),
+        if hidden:  # rows are outputs, as emb_gated_ffn_forward takes them
+            block = {"w_in": normal(experts, width, 2 * hidden).transpose(1, 2).contiguous(),
+                     "w_out": normal(experts, hidden, width).transpose(1, 2).contiguous()}
+        else:
+            block = {"experts": normal(experts, width, width)}
+        self.p = {"router": normal(width, experts), **block,
                   "gate": normal(width, 1).view(-1), "post": ones.clone(), "scale": 0.5 * ones,
                   "pre": ones.clone(), "head": normal(width, 1).view(-1)}
         # gradients, clipped in place
         self.g = {k: torch.zeros_like(v) for k, v in self.p.items()}
-        self.grads = eb.TensorList([self.g[k] for k in PARAMS])
+        self.grads = eb.TensorList([self.g[k] for k in self.names])
 
         def f(*shape, dtype=torch.float32):
             return torch.empty(shape, dtype=dtype, device=device)
@@ -69,8 +80,24 @@ class Model:
         need = max(eb.emb_expert_workspace_bytes(b, topk, experts),
                    eb.emb_gated_norm_workspace_bytes(b, width),
                    eb.emb_grad_workspace_bytes(self.grads))
+        if hidden:
+            self.ys, self.dxs = f(m, width), f(m, width)
+            self.gu, self.act = f(m, 2 * hidden), f(m, hidden)
+            need = max(need, eb.emb_gated_ffn_workspace_bytes(m, experts, width, hidden,
+                                                              eb.EMB_F32))
         self.ws = f(need, dtype=torch.uint8)
+        # seed and counter of the dropout's random words, of this step and the next
+        self.rng = torch.tensor([seed, 0], device=device)
         self.shape = (b, topk, m, width, eb.EMB_F32)
+
+    def ffn_shape(self):
+        return (self.rows_m, self.experts, self.capacity, self.width, self.hidden, eb.EMB_F32,
+                eb.EMB_ACT_SILU)
+
+    def drop(self, x):
+        """Dropout in place, of the block forward and of its gradient backward."""
+        eb.check(eb.emb_dropout(x, None, x.numel(), eb.EMB_F32, self.dropout, self.rng, x),
+                 "dropout")
 
     # ------------------------------------------------------------ forward
     def forward(self, offsets, ids):
@@ -88,9 +115,17 @@ class Model:
                                     self.ws.numel()), "sort")
         eb.check(eb.emb_expert_dispatch(self.x, self.pos, self.src, *self.shape, self.xs),
                  "dispatch")
-        self.ys = torch.bmm(self.xs.view(self.experts, self.capacity, self.width), p["experts"])
+        if self.hidden:
+            eb.check(eb.emb_gated_ffn_forward(self.xs, p["w_in"], p["w_out"], self.offsets,
+                                              *self.ffn_shape(), self.gu, self.act, self.ys,
+                                              self.ws, self.ws.numel()), "experts")
+        else:
+            self.ys = torch.bmm(self.xs.view(self.experts, self.capacity, self.width),
+                                p["experts"])
         eb.check(eb.emb_expert_combine(self.ys, self.pos, self.weight, *self.shape, self.block),
                  "combine")
+        if self.dropout:
+            self.drop(self.block)
         self.a = self.x @ p["gate"]
         eb.check(eb.emb_gated_norm_forward(self.x, self.block, self.a, p["post"], p["scale"],
                                            p["pre"], self.batch, self.width, eb.EMB_F32, GATE,
@@ -108,13 +143,22 @@ class Model:
             self.y, self.block, self.a, p["post"], p["scale"], p["pre"], dy, dh, self.batch,
             self.width, eb.EMB_F32, GATE, NORM_EPS, self.dx, self.dblock, self.dgate, g["post"],
             g["scale"], g["pre"], self.ws, self.ws.numel()), "norm backward")
+        if self.dropout:  # the forward's random words again
+            self.drop(self.dblock)
         eb.check(eb.emb_expert_combine_backward(self.dblock, self.ys, self.pos, self.src,
                                                 self.weight, *self.shape, self.dys, self.dchoice),
                  "combine backward")
-        dys = self.dys.view(e, self.capacity, self.width)
-        xs = self.xs.view(e, self.capacity, self.width)
-        torch.bmm(xs.transpose(1, 2).contiguous(), dys, out=g["experts"])
-        dxs = torch.bmm(dys, p["experts"].transpose(1, 2).contiguous())
+        if self.hidden:
+            dxs = self.dxs
+            eb.check(eb.emb_gated_ffn_backward(self.xs, self.gu, self.act, p["w_in"], p["w_out"],
+                                               self.dys, self.offsets, *self.ffn_shape(), dxs,
+                                               g["w_in"], g["w_out"], self.ws, self.ws.numel()),
+                     "experts backward")
+        else:
+            dys = self.dys.view(e, self.capacity, self.width)
+            xs = self.xs.view(e, self.capacity, self.width)
+            torch.bmm(xs.transpose(1, 2).contiguous(), dys, out=g["experts"])
+            dxs = torch.bmm(dys, p["experts"].transpose(1, 2).contiguous())
         eb.check(eb.emb_expert_dispatch_backward(dxs, self.pos, *self.shape, self.dtok),
                  "dispatch backward")
         # the router: through the softmax over the chosen logits
@@ -137,11 +181,12 @@ class Model:
                                                  self.table_ws, self.table_bytes), "reduce")
         eb.check(eb.emb_clip_grad_norm(self.grads, self.grads, self.sqnorm, 1, self.max_norm,
                                        self.norm, self.ws, self.ws.numel()), "clip")
-        for k in PARAMS:
+        for k in self.names:
             self.p[k].add_(self.g[k], alpha=-self.lr)
         eb.check(eb.emb_bag_adagrad_reduced_prepared(t.handle, self.batch, nnz, self.sums,
                                                      self.norm[1:], self.lr, ADAGRAD_EPS,
                                                      self.table_ws, self.table_bytes), "step")
+        self.rng[1] += (self.block.numel() + 3) // 4  # past this step's random words
         return loss, self.norm
 
     def close(self):
@@ -166,8 +211,10 @@ def main(argv=None):
     ap.add_argument("--batch", type=int, default=4096)
     ap.add_argument("--dim", type=int, default=64)
     ap.add_argument("--rows", type=int, nargs="+", default=[50, 200, 1000, 5000])
+    ap.add_argument("--hidden", type=int, default=0, help="of gated feed-forward experts")
+    ap.add_argument("--dropout", type=float, default=0.0)
     a = ap.parse_args(argv)
-    model = Model(a.rows, a.dim, a.batch)
+    model = Model(a.rows, a.dim, a.batch, hidden=a.hidden, dropout=a.dropout)
     losses = []
     for i in range(a.steps):
         loss, norm = model.step(*batch_of(a.rows, a.batch, i))

@@ -176,8 +176,9 @@ struct Cutter {
     c.width[i] = width;
     c.first[i + 1] = c.first[i] + dst.size / 8;
   }
+  template <class T>
   hipError_t launch(hipStream_t s) const {
-    hipLaunchKernelGGL(k_ffn_cut, row_grid((c.first[c.count] + 255) / 256), dim3(256), 0, s, c);
+    hipLaunchKernelGGL(k_ffn_cut<T>, row_grid((c.first[c.count] + 255) / 256), dim3(256), 0, s, c);
     return hipGetLastError();
   }
 };
@@ -259,6 +260,7 @@ hipError_t weight_gradients(const Groups& g, const T* dgu, const void* x, const 
 }
 
 // The forward and backward of fp32 through planes.
+template <class T>
 hipError_t forward_planes(const GatedFfn& f, void* gu, void* a, void* y, char* ws,
                           hipStream_t s) {
   const int64_t D = f.dim, F = f.hidden;
@@ -270,7 +272,7 @@ hipError_t forward_planes(const GatedFfn& f, void* gu, void* a, void* y, char* w
   cut.add(f.x, px, D);
   cut.add(f.w_in, pin, D);
   cut.add(f.w_out, pout, F);
-  hipError_t e = cut.launch(s);
+  hipError_t e = cut.launch<T>(s);
   if (e != hipSuccess) return e;
   e = rows_product_planes<true>(
       g, px, pin, F, 2 * F,
@@ -280,6 +282,7 @@ hipError_t forward_planes(const GatedFfn& f, void* gu, void* a, void* y, char* w
                                    StorePlanesEpilogue{{static_cast<float*>(y), D}}, s);
 }
 
+template <class T>
 hipError_t backward_planes(const GatedFfn& f, const void* gu, const void* a, const void* dy,
                            void* dx, void* dw_in, void* dw_out, char* ws, hipStream_t s) {
   const int64_t D = f.dim, F = f.hidden;
@@ -294,7 +297,7 @@ hipError_t backward_planes(const GatedFfn& f, const void* gu, const void* a, con
   cut.add(f.w_in, pin, D);
   cut.add(f.w_out, pout, F);
   cut.add(dy, pdy, D);
-  hipError_t e = cut.launch(s);
+  hipError_t e = cut.launch<T>(s);
   if (e != hipSuccess) return e;
   e = rows_product_planes<false>(
       g, pdy, pout, F, D,
@@ -304,7 +307,7 @@ hipError_t backward_planes(const GatedFfn& f, const void* gu, const void* a, con
                                  StorePlanesEpilogue{{static_cast<float*>(dx), D}}, s);
   if (e != hipSuccess) return e;
   const WeightPlanes planes{{pdgu, pdy}, {px, pa}};
-  return weight_gradients<float>(g, nullptr, f.x, dy, a, &planes, D, F, dw_in, dw_out,
+  return weight_gradients<T>(g, nullptr, f.x, dy, a, &planes, D, F, dw_in, dw_out,
                                  reinterpret_cast<float*>(space.at), s);
 }
 
@@ -334,7 +337,7 @@ hipError_t ffn_forward_t(const GatedFfn& f, void* gu, void* a, void* y, char* ws
   }
   if constexpr (sizeof(T) == 4)
     if (by_planes(f.rows, f.experts, F, kForwardPlanes))
-      return forward_planes(f, gu, a, y, ws, s);
+      return forward_planes<T>(f, gu, a, y, ws, s);
   const hipError_t e = rows_product<T, true>(g, f.x, f.w_in, D, F, 2 * F * D, middle, s);
   if (e != hipSuccess) return e;
   return rows_product<T, true>(g, a, f.w_out, F, D, D * F, end, s);
@@ -345,7 +348,7 @@ hipError_t ffn_backward_t(const GatedFfn& f, const void* gu, const void* a, cons
                           void* dx, void* dw_in, void* dw_out, char* ws, hipStream_t s) {
   if constexpr (sizeof(T) == 4)
     if (f.rows && by_planes(f.rows, f.experts, f.hidden, kBackwardPlanes))
-      return backward_planes(f, gu, a, dy, dx, dw_in, dw_out, ws, s);
+      return backward_planes<T>(f, gu, a, dy, dx, dw_in, dw_out, ws, s);
   const int64_t D = f.dim, F = f.hidden;
   const Groups g{f.offsets, f.rows, f.capacity, f.experts};
   T* dgu = reinterpret_cast<T*>(ws);

@@ -63,7 +63,8 @@ struct Cuts {
   int32_t count;
 };
 
-__global__ __launch_bounds__(256) inline void k_ffn_cut(const Cuts c) {
+template <class T>
+__global__ __launch_bounds__(256) void k_ffn_cut(const Cuts c) {
   const int64_t v = (int64_t)block_index() * 256 + threadIdx.x;
   if (v >= c.first[c.count]) return;
   int m = 0;
