@@ -187,7 +187,7 @@ template <bool B_KC, class Epilogue>
 hipError_t rows_product_planes(const Groups& g, const Planes& a, const Planes& b, int64_t N,
                                int64_t b_rows, const Epilogue& epilogue, hipStream_t s) {
   const int64_t cols = Epilogue::kDual ? kTileO / 2 : kTileO;
-  const int64_t col_tiles = (N + cols - 1) / cols;
+  const int64_t col_tiles = (epilogue.columns() + cols - 1) / cols;
   const int64_t blocks = blocks_of(row_tiles_bound(g, 128) * col_tiles, kRowChunk);
   // 64 rows a block where 128 leave CUs without one (4096 x 479 from 1000: 36 us
   // against 49)

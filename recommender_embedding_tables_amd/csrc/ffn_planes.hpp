@@ -105,14 +105,15 @@ __global__ __launch_bounds__(256) void k_ffn_cut(const Cuts c) {
 }
 
 // ---------------------------------------------------------------- epilogues
-// All also cover the columns that pad a row of planes.
+// All also cover the columns that pad a row of planes, which can begin a tile of their
+// own.
 struct ActPlanesEpilogue : ActEpilogue<float> {
   Planes planes;  // of a
   struct Row {
     ActEpilogue<float>::Row values;
     int64_t at;
   };
-  __device__ inline int64_t columns() const { return planes.ld; }
+  __host__ __device__ inline int64_t columns() const { return planes.ld; }
   __device__ inline Row row(int64_t r) const {
     return {ActEpilogue<float>::row(r), r * planes.ld};
   }
@@ -131,7 +132,7 @@ struct ActGradPlanesEpilogue : ActGradEpilogue<float> {
     ActGradEpilogue<float>::Row values;
     int64_t at;
   };
-  __device__ inline int64_t columns() const { return planes.ld - width; }
+  __host__ __device__ inline int64_t columns() const { return planes.ld - width; }
   __device__ inline Row row(int64_t r) const {
     return {ActGradEpilogue<float>::row(r), r * planes.ld};
   }
@@ -146,7 +147,7 @@ struct ActGradPlanesEpilogue : ActGradEpilogue<float> {
 };
 
 struct StorePlanesEpilogue : StoreEpilogue<float> {
-  __device__ inline int64_t columns() const { return width; }
+  __host__ __device__ inline int64_t columns() const { return width; }
   __device__ inline NothingHeld held4(const Row&, int64_t) const { return {}; }
   __device__ inline void store4(const Row& r, int64_t n, const float (&v)[4],
                                 const NothingHeld& h) const {

@@ -193,6 +193,96 @@ def test_backward(shape, kind):
     assert all(torch.equal(p, q) for p, q in zip(c.backward(), got))
 
 
+def ragged(experts, most, seed):
+    """Group sizes 0 .. most, an empty one among them."""
+    n = np.random.default_rng(seed).integers(0, most + 1, experts)
+    n[experts // 2] = 0
+    return [int(v) for v in n]
+
+
+# Sizes at which the rules on sizes choose another kernel: large and small tiles of
+# 16-bit values, whose widths end inside a slot, a half slot and a vector; parts of
+# the weights' rows; fp32 in tiles of its own values and through planes, in blocks of
+# 64 and 128 rows; one and more steps of experts in a wave.
+PATHS = {
+    "large": (ragged(20, 700, 1), 0, 3, 1032, 520),
+    "large_half_slot": (ragged(20, 700, 2), 0, 0, 288, 1056),
+    "large_odd_hidden": (ragged(20, 700, 3), 0, 1, 1032, 521),
+    "large_odd_width": (ragged(20, 700, 4), 0, 0, 1031, 520),
+    "large_capacity": (ragged(20, 400, 5), 400, 0, 776, 520),
+    "parts": ([600 + i for i in range(17)], 0, 9, 264, 132),
+    "tiles_fp32": ([900 - 3 * i for i in range(8)], 0, 5, 136, 520),
+    "planes_64": ([900, 0, 37], 0, 0, 136, 333),
+    "planes_128": ([1270], 0, 11, 72, 1400),
+    "planes_128_backward": ([2500], 0, 0, 40, 1200),
+    "experts_64": (ragged(64, 90, 6), 0, 2, 48, 40),
+    "experts_65": (ragged(65, 90, 7), 0, 2, 48, 40),
+}
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("path", list(PATHS))
+def test_kernels_of_every_size(path, kind):
+    c = Case(*PATHS[path], kind, "silu", seed=len(path))
+    got = c.forward()
+    c.check_forward(*got)
+    assert all(torch.equal(p, q) for p, q in zip(c.forward(), got))
+    got = c.backward()
+    c.check_backward(*got)
+    c.ws.fill_(7)
+    assert all(torch.equal(p, q) for p, q in zip(c.backward(), got))
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("hidden", list(range(119, 131)) + [253, 254, 255])
+def test_widths_at_the_end_of_a_tile(hidden, kind):
+    c = Case([300], 0, 0, 40, hidden, kind, "silu", dense=True)
+    c.check_forward(*c.forward())
+    c.check_backward(*c.backward())
+    c = Case([150, 70], 0, 0, hidden, 48, kind, "silu")
+    c.check_forward(*c.forward())
+    c.check_backward(*c.backward())
+
+
+@pytest.mark.parametrize("dim,hidden", [(16_384, 65_528), (32_768, 32_768)])
+def test_weights_of_two_gigabytes(dim, hidden):
+    """Offsets of 32 bits just reach (the first) or do not (the second)."""
+    t, rows = torch.bfloat16, 300
+    g = gen(12)
+    x = rand(g, rows, dim).to(t)
+    w_in = torch.empty(1, 2 * hidden, dim, dtype=t, device=DEV)
+    w_out = torch.empty(1, dim, hidden, dtype=t, device=DEV)
+    for w, k in ((w_in, dim), (w_out, hidden)):
+        for part in w[0].split(8192):
+            part.copy_(rand(g, *part.shape, scale=k ** -0.5))
+    gu, a, y = (torch.empty(rows, n, dtype=t, device=DEV) for n in (2 * hidden, hidden, dim))
+    need = eb.emb_gated_ffn_workspace_bytes(rows, 1, dim, hidden, eb.EMB_BF16)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    args = (rows, 1, 0, dim, hidden, eb.EMB_BF16, eb.EMB_ACT_SILU)
+    eb.check(eb.emb_gated_ffn_forward(x, w_in, w_out, None, *args, gu, a, y, ws, need), "forward")
+    dx, dw_in, dw_out = torch.empty_like(x), torch.empty_like(w_in), torch.empty_like(w_out)
+    eb.check(eb.emb_gated_ffn_backward(x, gu, a, w_in, w_out, y, None, *args, dx, dw_in, dw_out,
+                                       ws, need), "backward")
+
+    def product(p, q, what, got, k):
+        p, q = p.double(), q.double()
+        within(got, p @ q.t(), terms(k, t) * U * (p.abs() @ q.abs().t()), what)
+
+    ends = [0, 1, hidden - 1, hidden, 2 * hidden - 1]
+    product(x, w_in[0, ends], "gu", gu[:, ends], dim)
+    product(a, w_out[0, [0, dim - 1]], "y", y[:, [0, dim - 1]], hidden)
+    product(y.t()[[0, 7, dim - 1]], a.t(), "dw_out", dw_out[0, [0, 7, dim - 1]], rows)
+    # dgu of the last unit, then its weights' gradients and its share of dx
+    n = hidden - 1
+    da = y.double() @ w_out[0, :, n].double()
+    f, slope = act64("silu", gu[:, n].double())
+    dg, du = da * gu[:, hidden + n].double() * slope, da * f
+    for row, d in ((n, dg), (hidden + n, du)):
+        ref = d @ x.double()
+        err = float((dw_in[0, row].double() - ref).norm() / ref.norm())
+        assert err <= 4 * half(t)  # dgu's rounding and the result's
+
+
 @pytest.mark.parametrize("kind", list(TYPES))
 @pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("scale", [0.3, 8.0])
