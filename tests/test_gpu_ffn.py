@@ -364,6 +364,20 @@ def test_error_over_a_whole_matrix(kind):
     assert float((dw_out[0].double() - ref).norm()) <= lim * float(ref.norm())
 
 
+@pytest.mark.parametrize("rows", [5, 300])
+def test_subnormal_fp16_values_count(rows):
+    """x near 3e-6 is below fp16's normal range, and its products are kept."""
+    c = Case([rows], 0, 0, 264, 72, "f16", "silu", dense=True)
+    c.x.mul_(3e-6)
+    assert (c.x.float().abs() < 2.0 ** -14).all() and (c.x != 0).any()
+    c.w_in.mul_(100)
+    c.check_forward(*c.forward())
+    gu = c.forward()[0].double()
+    ref = c.x.double() @ c.w_in[0].double().t()
+    assert float((gu - ref).norm()) <= 2 * half(torch.float16) * float(ref.norm()) + \
+        2.0 ** -24 * gu.numel() ** 0.5
+
+
 @pytest.mark.parametrize("act", list(ACTS))
 def test_gradients_against_differences(act):
     """Of L = sum(y * dy) along a direction, beside what the difference itself is
