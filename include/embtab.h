@@ -719,10 +719,13 @@ emb_status_t emb_gated_norm_backward(const void* y, const void* block, const voi
  *          expert: every row is its
  *   rows, capacity  the buffer's M rows and the capacity of emb_expert_sort
  *          (rows = experts * capacity, or capacity 0)
- * The rows of no expert are neither read nor written.  The sums are in fp32;
+ * The rows of no expert count for nothing, whatever they hold, and are not
+ * written.  The sums are in fp32;
  * gu, a and y are rounded once each, and y is formed from the rounded a.  gu
- * and a are what the backward needs: gu NULL where it is not wanted.  An
- * infinite fp32 input gives NaN or an infinity.
+ * and a are what the backward needs: gu NULL where it is not wanted.  fp32
+ * values may enter the products as the sum of three bf16 parts, which hold all
+ * of them between 2^-100 and 3.38e38; a larger or infinite one leaves NaN or an
+ * infinity in the sums it enters, a smaller one loses its last bits.
  *
  * The backward takes gu and a as the forward stored them:
  *   da = Wo' dy;  du = da * act(g);  dg = da * u * act'(g)   (rounded to dtype)
@@ -732,9 +735,10 @@ emb_status_t emb_gated_norm_backward(const void* y, const void* block, const voi
  * each sum in fp32 and rounded once.  dw_in, dw_out: as the weights.
  *
  * 8 <= dim, hidden <= 65536; 1 <= experts <= 1024; rows * dim and rows * hidden
- * below 2^40.  Outputs must not overlap inputs or each other.  Offsets that are
- * not ascending inside [0, rows] give results without meaning, but no access
- * outside the buffers. */
+ * below 2^40.  Both directions take a workspace of emb_gated_ffn_workspace_bytes.
+ * Outputs must not overlap inputs or each other.  Offsets that are not ascending
+ * inside [0, rows] give results without meaning, but no access outside the
+ * buffers. */
 typedef enum {
   EMB_ACT_SILU = 0,    /* v / (1 + e^-v) */
   EMB_ACT_GELU = 1,    /* v (1 + erf(v / sqrt 2)) / 2 */

@@ -55,7 +55,9 @@ inline int64_t row_tiles_bound(const Groups& g, int64_t tile) {
 // of kPanel row tiles walk over the column tiles with the rows innermost.  Chunks
 // of 32 tiles (8 row and 4 column tiles), one for each CU of an XCD, where every
 // tile costs the same; weight gradients, whose tiles cost their expert's rows,
-// take chunks of 8.
+// take chunks of 8 and the longest expert first (32768 x 3328 x 1664 bf16, 16 experts
+// with 0.3 to 3 times the mean's rows: 1156 us for both matrices, in chunks of 32 by
+// expert 1463, with one run of tiles to each XCD 2125).
 constexpr uint32_t kXcds = 8, kPanel = 8;
 constexpr uint32_t kRowChunk = 32, kWeightChunk = 8;
 

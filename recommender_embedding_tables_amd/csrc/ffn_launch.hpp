@@ -81,8 +81,8 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 //   bf16  1 expert, 3328 x 1664: 256 rows 77, 99; 512 rows 149, 98
 //         8 experts, 512 x 1024: 64 rows each 19, 35; 128 34, 36; 256 59, 37
 //         32 experts, 1664 x 1024: 8 rows each 81, 85; 16 90, 85; 32 117, 87
-//   fp32  1 expert, 3328 x 1664: 128 rows 93, 130; 256 189, 131
-//         32 experts, 1664 x 1024: 16 rows each 188, 241; 32 249, 251; 64 402, 245
+//   fp32  1 expert, 3328 x 1664: 128 rows 80, 130; 256 189, 131
+//         32 experts, 1664 x 1024: 16 rows each 174, 241; 32 231, 251; 64 402, 245
 template <class T>
 bool by_few_rows(const Groups& g, int64_t hidden) {
   const int64_t passes = (g.rows + kFewRows * g.experts - 1) / (kFewRows * g.experts);
@@ -147,6 +147,11 @@ struct PlanesRule {
   int64_t long_blocks, long_rows;  // or up to this many, of experts with so many rows
 };
 constexpr PlanesRule kForwardPlanes{112, 256, 2048}, kBackwardPlanes{256, 512, 1024};
+// (the workspace is that of the backward)
+static_assert(kForwardPlanes.blocks <= kBackwardPlanes.blocks &&
+                  kForwardPlanes.long_blocks <= kBackwardPlanes.long_blocks &&
+                  kForwardPlanes.long_rows >= kBackwardPlanes.long_rows,
+              "a forward through planes has a workspace that holds them");
 bool by_planes(int64_t rows, int32_t experts, int64_t hidden, const PlanesRule& r) {
   // the groups' largest number of row tiles, whatever the capacity
   const int64_t used = rows < experts ? rows : experts;
