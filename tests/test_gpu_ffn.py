@@ -244,6 +244,13 @@ def test_widths_at_the_end_of_a_tile(hidden, kind):
     c.check_backward(*c.backward())
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("width", list(range(8, 34)) + list(range(248, 274)) + [513, 575, 767])
+def test_few_rows_of_widths_that_end_inside_a_vector(width, kind):
+    c = Case([3, 0, 19, 40], 0, 1, width, 2 * width - 7, kind, "silu")
+    c.check_forward(*c.forward())
+
+
 @pytest.mark.parametrize("dim,hidden", [(16_384, 65_528), (32_768, 32_768)])
 def test_weights_of_two_gigabytes(dim, hidden):
     """Offsets of 32 bits just reach (the first) or do not (the second)."""
