@@ -195,13 +195,19 @@ hipError_t rows_product_planes(const Groups& g, const Planes& a, const Planes& b
   const int64_t col_tiles = (epilogue.columns() + cols - 1) / cols;
   const int64_t blocks = blocks_of(row_tiles_bound(g, 128) * col_tiles, kRowChunk);
   // 64 rows a block where 128 leave CUs without one (4096 x 479 from 1000: 36 us
-  // against 49)
+  // against 49), and two such blocks a CU where the epilogue reads what it stores with,
+  // so that one's waits and stores hide behind the other (backward of 8 experts, 479 x
+  // 640, 1024 rows each, 262 us with 128 rows, 253; 1 expert, 479 x 1000, 4096 rows 207,
+  // 200; 3327 x 1663 1454, 1466)
+  const int64_t half = blocks_of(row_tiles_bound(g, 64) * col_tiles, kRowChunk);
   if (blocks <= 192) {
-    const int64_t half = blocks_of(row_tiles_bound(g, 64) * col_tiles, kRowChunk);
-    hipLaunchKernelGGL((k_ffn_rows_planes<B_KC, Epilogue, 64>), tile_grid(half, 256), dim3(256),
-                       0, s, g, a, b, N, b_rows, (uint32_t)col_tiles, epilogue);
+    hipLaunchKernelGGL((k_ffn_rows_planes<B_KC, Epilogue, 64, 4>), tile_grid(half, 256),
+                       dim3(256), 0, s, g, a, b, N, b_rows, (uint32_t)col_tiles, epilogue);
+  } else if constexpr (Epilogue::kReads) {
+    hipLaunchKernelGGL((k_ffn_rows_planes<B_KC, Epilogue, 64, 2>), tile_grid(half, 256),
+                       dim3(256), 0, s, g, a, b, N, b_rows, (uint32_t)col_tiles, epilogue);
   } else {
-    hipLaunchKernelGGL((k_ffn_rows_planes<B_KC, Epilogue, 128>), tile_grid(blocks, 512), dim3(512),
+    hipLaunchKernelGGL((k_ffn_rows_planes<B_KC, Epilogue, 128, 3>), tile_grid(blocks, 512), dim3(512),
                        0, s, g, a, b, N, b_rows, (uint32_t)col_tiles, epilogue);
   }
   return hipGetLastError();

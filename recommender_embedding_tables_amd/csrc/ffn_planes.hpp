@@ -111,8 +111,9 @@ __global__ __launch_bounds__(256) void k_ffn_cut(const Cuts c) {
 
 // ---------------------------------------------------------------- epilogues
 // All also cover the columns that pad a row of planes, which can begin a tile of their
-// own.
+// own.  kReads: whether it reads as much as it stores.
 struct ActPlanesEpilogue : ActEpilogue<float> {
+  static constexpr bool kReads = false;
   Planes planes;  // of a
   struct Row {
     ActEpilogue<float>::Row values;
@@ -132,6 +133,7 @@ struct ActPlanesEpilogue : ActEpilogue<float> {
 };
 
 struct ActGradPlanesEpilogue : ActGradEpilogue<float> {
+  static constexpr bool kReads = true;
   Planes planes;  // of dgu, which is not stored itself
   struct Row {
     ActGradEpilogue<float>::Row values;
@@ -152,6 +154,7 @@ struct ActGradPlanesEpilogue : ActGradEpilogue<float> {
 };
 
 struct StorePlanesEpilogue : StoreEpilogue<float> {
+  static constexpr bool kReads = false;
   __host__ __device__ inline int64_t columns() const { return width; }
   __device__ inline NothingHeld held4(const Row&, int64_t) const { return {}; }
   __device__ inline void store4(const Row& r, int64_t n, const float (&v)[4],
@@ -234,11 +237,11 @@ struct Fragments {
 };
 
 // Tiles of OM x 128 by waves of 64 x 32: 128 rows by eight waves and a ring of
-// three stages, 64 rows by four and a ring of four (144 KB of LDS either way).  A
-// stage holds 32 k of both operands' planes.
-template <bool A_KC, bool B_KC, int OM>
+// three stages, 64 rows by four and a ring of four (144 KB of LDS either way) or, two
+// blocks a CU, of two.  A stage holds 32 k of both operands' planes.
+template <bool A_KC, bool B_KC, int OM, int RING>
 struct PlaneProduct {
-  static constexpr int WM = OM / 64, WN = 4, kThreads = 64 * WM * WN, kRing = OM == 128 ? 3 : 4;
+  static constexpr int WM = OM / 64, WN = 4, kThreads = 64 * WM * WN, kRing = RING;
   static constexpr int FM = 4, FN = 2;
   typedef StageLoads<A_KC, OM, kThreads> LoadsA;
   typedef StageLoads<B_KC, kTileO, kThreads> LoadsB;
@@ -328,11 +331,11 @@ struct PlaneProduct {
 };
 
 // As k_ffn_rows, from planes: A [rows, K], B the expert's weights.
-template <bool B_KC, class Epilogue, int OM>
+template <bool B_KC, class Epilogue, int OM, int RING>
 __global__ __launch_bounds__(OM * 4) void k_ffn_rows_planes(
     const Groups groups, const Planes A, const Planes B, int64_t N, int64_t b_rows,
     uint32_t col_tiles, const Epilogue epilogue) {
-  typedef PlaneProduct<true, B_KC, OM> Product;
+  typedef PlaneProduct<true, B_KC, OM, RING> Product;
   constexpr int FM = Product::FM, FN = Product::FN;
   __shared__ __attribute__((aligned(16))) uint16_t lds[Product::kRing * Product::kStage / 2];
   constexpr int kCols = Epilogue::kDual ? kTileO / 2 : kTileO;
@@ -404,7 +407,7 @@ struct WeightPlanes {
 template <class Out, int OM>
 __global__ __launch_bounds__(OM * 4) void k_ffn_weights_planes(
     const WeightProducts<float> w, const WeightPlanes planes, const WeightEpilogue<Out> out) {
-  typedef PlaneProduct<false, false, OM> Product;
+  typedef PlaneProduct<false, false, OM, 3> Product;
   constexpr int FM = Product::FM, FN = Product::FN;
   __shared__ __attribute__((aligned(16))) uint16_t lds[Product::kRing * Product::kStage / 2];
   WeightTile t;
