@@ -10,9 +10,10 @@
 // its own, and the four lanes of a row read a line together.  fp32 takes the fp32
 // matrix instructions, which keep up with the memory at these rows.
 //
-// 64 rows that use 18 of 32 experts, 3328 x 1664 bf16: 390 and 168 MB of weights in 72
-// and 41 us (5.4 and 4.1 TB/s); 16 rows of 8 experts, 512 x 1024: 6.3 and 5.2 us, which
-// are a few dependent waits.
+// 64 rows that use 15 of 32 experts, 3328 x 1664 bf16: 336 and 168 MB of weights in 71
+// and 39 us (4.7 and 4.3 TB/s); 18 experts 72 and 41 us (the blocks' last round is
+// fuller); 16 rows of 8 experts, 512 x 1024: 6.3 and 5.2 us, which are a few dependent
+// waits.
 #pragma once
 
 #include "ffn.hpp"
