@@ -80,7 +80,8 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 // forward, this kernel against tiles):
 //   bf16  1 expert, 3328 x 1664: 256 rows 77, 99; 512 rows 149, 98
 //         8 experts, 512 x 1024: 64 rows each 19, 35; 128 34, 36; 256 59, 37
-//         32 experts, 1664 x 1024: 8 rows each 81, 85; 16 90, 85; 32 117, 87
+//         32 experts, 1664 x 1024: 8 rows each 76, 88; 16 85, 88; 32 107, 91
+//         24 experts, 3328 x 1664: 16 rows each 194, 269; 32 255, 272; 48 326, 276
 //   fp32  1 expert, 3328 x 1664: 128 rows 80, 130; 256 189, 131
 //         32 experts, 1664 x 1024: 16 rows each 174, 241; 32 231, 251; 64 402, 245
 template <class T>
