@@ -133,31 +133,39 @@ hipError_t rows_product(const Groups& g, const void* a, const void* b, int64_t K
   return hipGetLastError();
 }
 
-// Whether fp32 goes through planes: while the middle has few blocks of 128 x 128 (of
-// tiles that cut their own values several on a CU hide each other's waits), more of
-// them where many rows share an expert's planes (us, planes against those tiles):
-//   forward   1 expert, 3327 x 1663: 1024 rows (104 blocks) 212, 288
-//             1 expert, 479 x 1000: 4096 rows (256 blocks) 99, 112
-//             16 experts, 479 x 640: 128 rows each (80 blocks) 70, 73; 256 (160) 101, 88
-//   backward  1 expert, 3327 x 1663: 1024 rows 398, 648; 4096 (416 blocks) 1410, 1642
-//             16 experts, 479 x 640: 256 rows each (160 blocks) 174, 195; 512 (320) 295, 256
-//             8 experts, 479 x 640: 1024 rows each (320 blocks) 250, 252
-//             32 experts, 1664 x 1024: 8 rows each (256 blocks) 841, 475
-struct PlanesRule {
-  int64_t blocks;                  // fewer than this
-  int64_t long_blocks, long_rows;  // or up to this many, of experts with so many rows
-};
-constexpr PlanesRule kForwardPlanes{112, 256, 2048}, kBackwardPlanes{256, 512, 1024};
-// (the workspace is that of the backward)
-static_assert(kForwardPlanes.blocks <= kBackwardPlanes.blocks &&
-                  kForwardPlanes.long_blocks <= kBackwardPlanes.long_blocks &&
-                  kForwardPlanes.long_rows >= kBackwardPlanes.long_rows,
-              "a forward through planes has a workspace that holds them");
-bool by_planes(int64_t rows, int32_t experts, int64_t hidden, const PlanesRule& r) {
-  // the groups' largest number of row tiles, whatever the capacity
+// Whether fp32 goes through planes.  Planes save waits along k: a product of tiles that
+// cut their own values takes 0.8 (forward) to 1.3 us for every 32 k while one block
+// is alone on its CU, and several blocks hide each other's.  Planes cost the cutting of
+// every weight, of experts without rows too, and its reading with 6 bytes for 4: 2.6 to
+// 2.9 us for a million.  So they are taken while the weights are few for the k that the
+// products walk along, and their tiles too few to hide the waits (us, planes against tiles):
+//   forward   8 experts, 1664 x 640: 128 rows each 111, 130 (3700 weights a k); 1664 x
+//             1024 201, 151 (5070)
+//             1 expert, 479 x 1000: 2048 rows (320 tiles) 70, 95; 4096 (640) 101, 115;
+//             8192 (1280) 174, 167; 1664 x 640: 2048 rows (368) 126, 133; 4096 (736)
+//             211, 202; 4 experts, 1664 x 640: 1024 rows each (805) 231, 203
+//             4 experts, 128 x 256 (384 k): 1024 rows each (175) 29, 34; 2048 (335) 36, 35
+//   backward  8 experts, 1664 x 1024: 8 rows each 221, 275 (3670 weights a k); 3327 x 1663
+//             679, 594 (6650); 32 experts, 479 x 640: 8 rows each 175, 163 (5580); 1664 x
+//             640 532, 359 (11600)
+//             4 experts, 479 x 1000: 1024 rows each (280 blocks) 197, 307; 8 experts, 479 x
+//             640: 1024 (355) 251, 274; 16 experts (2790 weights a k): 256 (235) 192, 207;
+//             512 (395) 297, 286
+//             4 experts, 128 x 256 (640 k): 2048 rows each (134) 72, 94; 4096 (262) 115, 113
+int64_t row_tiles_128(int64_t rows, int32_t experts) {  // whatever the capacity
   const int64_t used = rows < experts ? rows : experts;
-  const int64_t blocks = (rows + used * 127) / 128 * ((hidden + 127) / 128);
-  return blocks < r.blocks || (blocks <= r.long_blocks && rows >= r.long_rows * experts);
+  return (rows + used * 127) / 128;
+}
+bool forward_by_planes(int64_t rows, int32_t experts, int64_t dim, int64_t hidden) {
+  const int64_t k = dim + hidden;
+  const int64_t tiles = row_tiles_128(rows, experts) * ((hidden + 63) / 64 + (dim + 127) / 128);
+  return rows > 0 && experts * dim * hidden <= 4000 * k && tiles <= 780 && 10 * tiles <= 7 * k;
+}
+bool backward_by_planes(int64_t rows, int32_t experts, int64_t dim, int64_t hidden) {
+  const int64_t k = dim + 2 * hidden, weights = experts * dim * hidden;
+  const int64_t blocks = row_tiles_128(rows, experts) * ((hidden + 127) / 128);  // of the middle
+  return rows > 0 && weights <= 4500 * k &&
+         (blocks <= 256 || (blocks <= 512 && weights <= 2500 * k && k >= 1500));
 }
 
 // Hands out the workspace from its start.
@@ -325,14 +333,23 @@ hipError_t backward_planes(const GatedFfn& f, const void* gu, const void* a, con
 
 }  // namespace
 
+// Planes of x, a and the weights, which both directions hold first.
+inline size_t forward_planes_bytes(int64_t rows, int32_t experts, int64_t dim, int64_t hidden) {
+  return planes_bytes(rows, dim) + planes_bytes(rows, hidden) +
+         planes_bytes(experts * 2 * hidden, dim) + planes_bytes(experts * dim, hidden);
+}
+
 template <class T>
 size_t ffn_workspace_bytes_t(int64_t rows, int32_t experts, int64_t dim, int64_t hidden) {
-  size_t n = dgu_bytes(rows, hidden, sizeof(T));
-  if (sizeof(T) == 4 && by_planes(rows, experts, hidden, kBackwardPlanes))
-    n = 2 * planes_bytes(rows, dim) + planes_bytes(rows, hidden) +
-        planes_bytes(rows, 2 * hidden) + planes_bytes(experts * 2 * hidden, dim) +
-        planes_bytes(experts * dim, hidden);
-  return n + parts_bytes(rows, experts, dim, hidden) + 256;
+  size_t forward = 0, backward = dgu_bytes(rows, hidden, sizeof(T));
+  if (sizeof(T) == 4) {
+    const size_t both = forward_planes_bytes(rows, experts, dim, hidden);
+    if (forward_by_planes(rows, experts, dim, hidden)) forward = both;
+    if (backward_by_planes(rows, experts, dim, hidden))
+      backward = both + planes_bytes(rows, dim) + planes_bytes(rows, 2 * hidden);
+  }
+  backward += parts_bytes(rows, experts, dim, hidden);
+  return (forward > backward ? forward : backward) + 256;
 }
 
 template <class T>
@@ -348,7 +365,7 @@ hipError_t ffn_forward_t(const GatedFfn& f, void* gu, void* a, void* y, char* ws
     return few_rows_product<T>(g, a, f.w_out, F, D, D * F, end, s);
   }
   if constexpr (sizeof(T) == 4)
-    if (by_planes(f.rows, f.experts, F, kForwardPlanes))
+    if (forward_by_planes(f.rows, f.experts, D, F))
       return forward_planes<T>(f, gu, a, y, ws, s);
   const hipError_t e = rows_product<T, true>(g, f.x, f.w_in, D, F, 2 * F * D, middle, s);
   if (e != hipSuccess) return e;
@@ -359,7 +376,7 @@ template <class T>
 hipError_t ffn_backward_t(const GatedFfn& f, const void* gu, const void* a, const void* dy,
                           void* dx, void* dw_in, void* dw_out, char* ws, hipStream_t s) {
   if constexpr (sizeof(T) == 4)
-    if (f.rows && by_planes(f.rows, f.experts, f.hidden, kBackwardPlanes))
+    if (backward_by_planes(f.rows, f.experts, f.dim, f.hidden))
       return backward_planes<T>(f, gu, a, dy, dx, dw_in, dw_out, ws, s);
   const int64_t D = f.dim, F = f.hidden;
   const Groups g{f.offsets, f.rows, f.capacity, f.experts};
