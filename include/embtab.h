@@ -735,10 +735,13 @@ emb_status_t emb_gated_norm_backward(const void* y, const void* block, const voi
  * each sum in fp32 and rounded once.  dw_in, dw_out: as the weights.
  *
  * 8 <= dim, hidden <= 65536; 1 <= experts <= 1024; rows * dim and rows * hidden
- * below 2^40.  Both directions take a workspace of emb_gated_ffn_workspace_bytes.
- * Outputs must not overlap inputs or each other.  Offsets that are not ascending
- * inside [0, rows] give results without meaning, but no access outside the
- * buffers. */
+ * below 2^40.  The backward, and a forward that keeps gu for it, take a
+ * workspace of emb_gated_ffn_workspace_bytes.  A forward without gu (serving)
+ * takes one of emb_gated_ffn_forward_workspace_bytes: 256 bytes, or the bf16
+ * parts of fp32 rows and weights where they are cut once for the call.
+ * Outputs must not overlap inputs or each other.  Offsets that are not
+ * ascending inside [0, rows] give results without meaning, but no access
+ * outside the buffers. */
 typedef enum {
   EMB_ACT_SILU = 0,    /* v / (1 + e^-v) */
   EMB_ACT_GELU = 1,    /* v (1 + erf(v / sqrt 2)) / 2 */
@@ -747,6 +750,8 @@ typedef enum {
 } emb_act_t;
 size_t emb_gated_ffn_workspace_bytes(int64_t rows, int32_t experts, int32_t dim, int32_t hidden,
                                      int32_t dtype);
+size_t emb_gated_ffn_forward_workspace_bytes(int64_t rows, int32_t experts, int32_t dim,
+                                             int32_t hidden, int32_t dtype);
 emb_status_t emb_gated_ffn_forward(const void* x, const void* w_in, const void* w_out,
                                    const int32_t* offsets, int64_t rows, int32_t experts,
                                    int64_t capacity, int32_t dim, int32_t hidden, int32_t dtype,

@@ -183,7 +183,9 @@ struct GatedFfn {
   int64_t rows, capacity;
   int32_t experts, dim, hidden, act;
 };
-template <class T>
+template <class T>  // what the forward itself uses
+size_t ffn_forward_workspace_bytes_t(int64_t rows, int32_t experts, int64_t dim, int64_t hidden);
+template <class T>  // of both directions
 size_t ffn_workspace_bytes_t(int64_t rows, int32_t experts, int64_t dim, int64_t hidden);
 template <class T>
 hipError_t ffn_forward_t(const GatedFfn& f, void* gu, void* a, void* y, char* ws, hipStream_t s);

@@ -84,6 +84,15 @@ size_t ffn_workspace(int64_t rows, int32_t experts, int32_t dim, int32_t hidden,
   }
 }
 
+size_t ffn_forward_workspace(int64_t rows, int32_t experts, int32_t dim, int32_t hidden,
+                             int32_t dtype) {
+  switch (dtype) {
+    case EMB_F32: return ffn_forward_workspace_bytes_t<float>(rows, experts, dim, hidden);
+    case EMB_BF16: return ffn_forward_workspace_bytes_t<bf16_t>(rows, experts, dim, hidden);
+    default: return ffn_forward_workspace_bytes_t<f16_t>(rows, experts, dim, hidden);
+  }
+}
+
 }  // namespace
 
 extern "C" {
@@ -227,6 +236,12 @@ size_t emb_gated_ffn_workspace_bytes(int64_t rows, int32_t experts, int32_t dim,
   return ffn_workspace(rows, experts, dim, hidden, dtype);
 }
 
+size_t emb_gated_ffn_forward_workspace_bytes(int64_t rows, int32_t experts, int32_t dim,
+                                             int32_t hidden, int32_t dtype) {
+  if (!ffn_shape_ok(rows, experts, dim, hidden, dtype)) return 0;
+  return ffn_forward_workspace(rows, experts, dim, hidden, dtype);
+}
+
 emb_status_t emb_gated_ffn_forward(const void* x, const void* w_in, const void* w_out,
                                    const int32_t* offsets, int64_t rows, int32_t experts,
                                    int64_t capacity, int32_t dim, int32_t hidden, int32_t dtype,
@@ -237,8 +252,9 @@ emb_status_t emb_gated_ffn_forward(const void* x, const void* w_in, const void* 
   const size_t al = dtype_size(dtype);
   if (!aligned(gu, al) || !data_ok(a, rows, al) || !data_ok(y, rows, al))
     return EMB_ERR_INVALID_ARG;
-  if (!workspace_ok(ws, ws_bytes, ffn_workspace(rows, experts, dim, hidden, dtype)))
-    return EMB_ERR_WORKSPACE;
+  const size_t need = gu ? ffn_workspace(rows, experts, dim, hidden, dtype)
+                         : ffn_forward_workspace(rows, experts, dim, hidden, dtype);
+  if (!workspace_ok(ws, ws_bytes, need)) return EMB_ERR_WORKSPACE;
   char* w = static_cast<char*>(ws);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   switch (dtype) {

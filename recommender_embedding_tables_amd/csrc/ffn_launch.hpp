@@ -85,10 +85,10 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 //   fp32  1 expert, 3328 x 1664: 128 rows 80, 130; 256 189, 131
 //         32 experts, 1664 x 1024: 16 rows each 174, 241; 32 231, 251; 64 402, 245
 template <class T>
-bool by_few_rows(const Groups& g, int64_t hidden) {
-  const int64_t passes = (g.rows + kFewRows * g.experts - 1) / (kFewRows * g.experts);
-  const int64_t tiles = g.experts * ((hidden + 127) / 128);
-  return g.rows <= (sizeof(T) == 2 ? 16 : 32) * (int64_t)g.experts ||
+bool by_few_rows(int64_t rows, int32_t experts, int64_t hidden) {
+  const int64_t passes = (rows + kFewRows * experts - 1) / (kFewRows * experts);
+  const int64_t tiles = experts * ((hidden + 127) / 128);
+  return rows <= (sizeof(T) == 2 ? 16 : 32) * (int64_t)experts ||
          passes * tiles <= (passes == 1 ? 128 : sizeof(T) == 2 ? 64 : 40);
 }
 
@@ -340,16 +340,22 @@ inline size_t forward_planes_bytes(int64_t rows, int32_t experts, int64_t dim, i
 }
 
 template <class T>
+size_t ffn_forward_workspace_bytes_t(int64_t rows, int32_t experts, int64_t dim,
+                                     int64_t hidden) {
+  const bool planes = sizeof(T) == 4 && !by_few_rows<T>(rows, experts, hidden) &&
+                      forward_by_planes(rows, experts, dim, hidden);
+  return (planes ? forward_planes_bytes(rows, experts, dim, hidden) : 0) + 256;
+}
+
+template <class T>
 size_t ffn_workspace_bytes_t(int64_t rows, int32_t experts, int64_t dim, int64_t hidden) {
-  size_t forward = 0, backward = dgu_bytes(rows, hidden, sizeof(T));
-  if (sizeof(T) == 4) {
-    const size_t both = forward_planes_bytes(rows, experts, dim, hidden);
-    if (forward_by_planes(rows, experts, dim, hidden)) forward = both;
-    if (backward_by_planes(rows, experts, dim, hidden))
-      backward = both + planes_bytes(rows, dim) + planes_bytes(rows, 2 * hidden);
-  }
-  backward += parts_bytes(rows, experts, dim, hidden);
-  return (forward > backward ? forward : backward) + 256;
+  const size_t forward = ffn_forward_workspace_bytes_t<T>(rows, experts, dim, hidden);
+  size_t backward = dgu_bytes(rows, hidden, sizeof(T));
+  if (sizeof(T) == 4 && backward_by_planes(rows, experts, dim, hidden))
+    backward = forward_planes_bytes(rows, experts, dim, hidden) + planes_bytes(rows, dim) +
+               planes_bytes(rows, 2 * hidden);
+  backward += parts_bytes(rows, experts, dim, hidden) + 256;
+  return forward > backward ? forward : backward;
 }
 
 template <class T>
@@ -359,7 +365,7 @@ hipError_t ffn_forward_t(const GatedFfn& f, void* gu, void* a, void* y, char* ws
   const ActEpilogue<T> middle{static_cast<T*>(gu), static_cast<T*>(a), F, f.act};
   const StoreEpilogue<T> end{static_cast<T*>(y), D};
   if (g.rows == 0) return hipSuccess;
-  if (by_few_rows<T>(g, F)) {
+  if (by_few_rows<T>(f.rows, f.experts, F)) {
     const hipError_t e = few_rows_product<T>(g, f.x, f.w_in, D, F, 2 * F * D, middle, s);
     if (e != hipSuccess) return e;
     return few_rows_product<T>(g, a, f.w_out, F, D, D * F, end, s);
@@ -393,6 +399,7 @@ hipError_t ffn_backward_t(const GatedFfn& f, const void* gu, const void* a, cons
 }
 
 #define EMBTAB_FFN_TYPE(T)                                                                     \
+  template size_t ffn_forward_workspace_bytes_t<T>(int64_t, int32_t, int64_t, int64_t);        \
   template size_t ffn_workspace_bytes_t<T>(int64_t, int32_t, int64_t, int64_t);                \
   template hipError_t ffn_forward_t<T>(const GatedFfn&, void*, void*, void*, char*,            \
                                        hipStream_t);                                           \

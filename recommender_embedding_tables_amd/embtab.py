@@ -67,7 +67,8 @@ EXPORTED = [
     "emb_expert_workspace_bytes", "emb_expert_sort", "emb_expert_dispatch", "emb_expert_combine",
     "emb_expert_combine_backward", "emb_expert_dispatch_backward",
     "emb_gated_norm_workspace_bytes", "emb_gated_norm_forward", "emb_gated_norm_backward",
-    "emb_gated_ffn_workspace_bytes", "emb_gated_ffn_forward", "emb_gated_ffn_backward",
+    "emb_gated_ffn_workspace_bytes", "emb_gated_ffn_forward_workspace_bytes",
+    "emb_gated_ffn_forward", "emb_gated_ffn_backward",
     "emb_add_norm_int8", "emb_expert_dispatch_int8", "emb_dropout",
 ]
 
@@ -193,6 +194,7 @@ def _load():
         "emb_gated_norm_backward": (i32, [P, P, P, P, P, P, P, P, i64, i32, i32, i32, f32, P, P,
                                           P, P, P, P, P, sz, P]),
         "emb_gated_ffn_workspace_bytes": (sz, [i64, i32, i32, i32, i32]),
+        "emb_gated_ffn_forward_workspace_bytes": (sz, [i64, i32, i32, i32, i32]),
         "emb_gated_ffn_forward": (i32, [P, P, P, P, i64, i32, i64, i32, i32, i32, i32, P, P, P,
                                         P, sz, P]),
         "emb_gated_ffn_backward": (i32, [P, P, P, P, P, P, P, i64, i32, i64, i32, i32, i32, i32,
@@ -680,6 +682,11 @@ def emb_gated_norm_backward(y, block, gate, w_post, scale, w_pre, dy, dh, rows, 
 
 def emb_gated_ffn_workspace_bytes(rows, experts, dim, hidden, dtype) -> int:
     return int(_lib.emb_gated_ffn_workspace_bytes(rows, experts, dim, hidden, dtype))
+
+
+def emb_gated_ffn_forward_workspace_bytes(rows, experts, dim, hidden, dtype) -> int:
+    """What a forward without gu takes."""
+    return int(_lib.emb_gated_ffn_forward_workspace_bytes(rows, experts, dim, hidden, dtype))
 
 
 def emb_gated_ffn_forward(x, w_in, w_out, offsets, rows, experts, capacity, dim, hidden, dtype,
