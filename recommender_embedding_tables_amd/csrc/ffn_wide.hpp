@@ -52,11 +52,15 @@ __device__ inline void load_to_lds(const char* base, uint32_t offset, uint32_t l
                "v"(offset), "s"(base)
                : "m0");
 }
+// The hardware wants five wait states between a vector instruction that writes a scalar
+// register and a load that reads it, and the compiler, which keeps them between its own
+// instructions, does not look into assembly.
 template <class P>
 __device__ inline const P* common_pointer(const P* p) {
   const uint64_t a = (uint64_t)(uintptr_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  asm volatile("s_nop 4" : "+s"(lo), "+s"(hi));
   return reinterpret_cast<const P*>((uintptr_t)(((uint64_t)hi << 32) | lo));
 }
 
