@@ -720,12 +720,14 @@ emb_status_t emb_gated_norm_backward(const void* y, const void* block, const voi
  *   rows, capacity  the buffer's M rows and the capacity of emb_expert_sort
  *          (rows = experts * capacity, or capacity 0)
  * The rows of no expert count for nothing, whatever they hold, and are not
- * written.  The sums are in fp32;
- * gu, a and y are rounded once each, and y is formed from the rounded a.  gu
- * and a are what the backward needs: gu NULL where it is not wanted.  fp32
- * values may enter the products as the sum of three bf16 parts, which hold all
- * of them between 2^-100 and 3.38e38; a larger or infinite one leaves NaN or an
- * infinity in the sums it enters, a smaller one loses its last bits.
+ * written.  The sums are in fp32; gu, a and y are rounded once each, and y is
+ * formed from the rounded a.  gu and a are what the backward needs: gu NULL
+ * where it is not wanted.  In fp16 a stored value beyond 65504 is infinite,
+ * whatever y would be, and one below 2^-25 is 0; the backward's dg and du
+ * likewise.  fp32 values enter a forward of few rows as they are, and all other
+ * products as the sum of three bf16 parts, which hold all of them between
+ * 2^-100 and 3.38e38: there a larger or infinite one leaves NaN or an infinity
+ * in the sums it enters, and a smaller one loses its last bits.
  *
  * The backward takes gu and a as the forward stored them:
  *   da = Wo' dy;  du = da * act(g);  dg = da * u * act'(g)   (rounded to dtype)
@@ -773,8 +775,9 @@ emb_status_t emb_gated_ffn_backward(const void* x, const void* gu, const void* a
  * the scheme of emb_quantize_rows_int8.  x, block, y: [rows, dim] of `dtype`;
  * w: fp32 [dim]; codes: int8 [rows, dim], any alignment; scales: fp32 [rows].
  * A row that holds a value that is not finite, or whose sum of squares is not,
- * has codes 0 and a NaN for its scale.  y may be x or block; other outputs must
- * not overlap inputs or each other.  eps >= 0.  The gradients, with the rounding
+ * has codes 0 and a NaN for its scale; with eps 0 so has one whose squares all
+ * vanish in fp32 (0 times the root's infinity).  y may be x or block; other
+ * outputs must not overlap inputs or each other.  eps >= 0.  The gradients, with the rounding
  * to 8 bits passed over, are those of emb_gated_norm_backward from y, without a
  * gate and w_post and with scale 1. */
 emb_status_t emb_add_norm_int8(const void* x, const void* block, const float* w, int64_t rows,

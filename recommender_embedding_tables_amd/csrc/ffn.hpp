@@ -206,7 +206,7 @@ inline dim3 tile_grid(int64_t blocks, int threads) {
 // e^-v as 2 to the power of -v log2(e) by the hardware.  The product's rounding
 // would be |v| 2^-24 of the result: below 16-bit data's own rounding, while fp32
 // takes it up again, e = the product's error with log2(e)'s second half, as
-// 2^(p + e) = 2^p (1 + e ln 2) within 2^-40.  1 / (1 + t) by the hardware's
+// 2^(p + e) = 2^p (1 + e ln 2) within 2^-37 (|e| < 2^-17).  1 / (1 + t) by the hardware's
 // reciprocal (1 ulp), for fp32 with one Newton step below 2^126.  The hardware gives 0
 // for results below 2^-126.
 template <class T>

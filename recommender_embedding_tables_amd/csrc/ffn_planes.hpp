@@ -7,7 +7,7 @@
 // value, rows padded with zeros to a multiple of 8, so that any width and
 // alignment will do), the products' results leave theirs as they are stored, and
 // the tiles load planes straight into LDS, three or four stages ahead, which a block
-// alone on its CU needs.  The six products and their order are those of ffn_tiles.hpp.
+// alone on its CU needs, or two where two blocks share one.  The six products and their order are those of ffn_tiles.hpp.
 //
 // 4096 x 479 from 1000: 36 us (the tiles above 50), forward of that size 99 us, of
 // which the outputs' and planes' 92 MB are 15; a stage takes 1.0 to 1.2 us where its
@@ -68,6 +68,7 @@ struct Cuts {
   int32_t count;
 };
 
+// (a template, so that of the sources that include this only the fp32 one holds it)
 template <class T>
 __global__ __launch_bounds__(256) void k_ffn_cut(const Cuts c) {
   const int64_t v = (int64_t)block_index() * 256 + threadIdx.x;

@@ -7,9 +7,10 @@
 //   to the input   A = dy, dgu (KC)   B = the weights [k, n] (OC)
 //   weights        A = dgu, dy (OC)   B = x, a (OC), k over the expert's rows
 // 16-bit values go to the matrix instructions as they are.  An fp32 value is the
-// exact sum of three bf16 (8 bits each, rounded to nearest), and of the nine
-// products the six down to 2^-18 are taken, the smaller ones first: what is left
-// out is below 2^-26 of a product, and the sums are in fp32.  That runs at a
+// exact sum of three bf16 (8 bits each, rounded to nearest, so that the second is
+// up to 2^-8 of the value and the third up to 2^-17), and of the nine products the
+// six that can reach 2^-17 are taken, the smaller ones first: what is left out is
+// below 2^-24 of a product, and the sums are in fp32.  That runs at a
 // sixth of the bf16 rate, 2.6 times that of the fp32 matrix instructions.  (An
 // infinite fp32 value leaves NaN in its sums.)
 //

@@ -1,7 +1,8 @@
 // Grouped matrix products of 16-bit values in tiles of 256 x 256, for gfx950.
 //
-// Bound by the matrix instructions, which keep the card at its power limit, and by
-// the way from L2 into LDS (10 TB/s in these kernels): the largest tile that eight
+// Bound by the matrix instructions, which take three quarters of the time by
+// themselves and keep the card at its power limit, and by what of the way from L2
+// into LDS (10 TB/s in these kernels) they do not hide: the largest tile that eight
 // waves hold in registers (128 x 64 results each) moves the fewest bytes, and both
 // operands go from memory straight into LDS, in lines of 128 bytes.  (In stages of
 // 32 k, with 64 bytes of a row at a time, L2 serves twice the requests for the same
