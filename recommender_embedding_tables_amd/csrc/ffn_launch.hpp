@@ -180,6 +180,11 @@ struct Space {
 size_t planes_bytes(int64_t rows, int64_t width) {
   return align256((size_t)rows * padded(width) * 6);
 }
+// Planes of x, a and the weights, which both directions hold first.
+size_t forward_planes_bytes(int64_t rows, int32_t experts, int64_t dim, int64_t hidden) {
+  return planes_bytes(rows, dim) + planes_bytes(rows, hidden) +
+         planes_bytes(experts * 2 * hidden, dim) + planes_bytes(experts * dim, hidden);
+}
 
 struct Cutter {
   Cuts c{};
@@ -332,12 +337,6 @@ hipError_t backward_planes(const GatedFfn& f, const void* gu, const void* a, con
 }
 
 }  // namespace
-
-// Planes of x, a and the weights, which both directions hold first.
-inline size_t forward_planes_bytes(int64_t rows, int32_t experts, int64_t dim, int64_t hidden) {
-  return planes_bytes(rows, dim) + planes_bytes(rows, hidden) +
-         planes_bytes(experts * 2 * hidden, dim) + planes_bytes(experts * dim, hidden);
-}
 
 template <class T>
 size_t ffn_forward_workspace_bytes_t(int64_t rows, int32_t experts, int64_t dim,
